@@ -488,3 +488,11 @@ def probe_xcd(workgroups, full_lds=True, spin_cycles=0, stream=None):
     if rc != HKG_OK:
         raise HkgError(rc, "hkg_probe_xcd")
     return out
+
+
+# ---- MXFP4 linear layer (include/hkg_ops.h) -------------------------------------------
+
+HKG_ERR_WORKSPACE = -9
+
+from .ops import (gemm_mxfp4, linear_mxfp4, linear_mxfp4_backward,  # noqa: E402,F401
+                  mxfp4_dequantize, mxfp4_quantize, mxfp4_quantize_both)

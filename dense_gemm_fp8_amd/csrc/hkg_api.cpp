@@ -468,6 +468,7 @@ const char *hkg_status_string(int status)
     case HKG_ERR_DEVICE: return "the stream's device is not a gfx950, or could not be queried";
     case HKG_ERR_LAUNCH: return "kernel launch failed";
     case HKG_ERR_OVERLAP: return "an output overlaps an input or the other output";
+    case HKG_ERR_WORKSPACE: return "workspace smaller than the call needs";
     default: return "unknown status";
     }
 }

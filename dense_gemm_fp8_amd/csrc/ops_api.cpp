@@ -1,0 +1,338 @@
+// ops_api.cpp -- entry points of the MXFP4 linear layer (hkg_ops.h): argument
+// checks, workspace layout and launches.  As in hkg_api.cpp every check runs
+// before the first HIP call.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ops_internal.h"
+#include "ops_kernels.h"
+
+namespace hkg::api {
+namespace {
+
+struct Range {
+    const void *p;
+    int64_t n;
+};
+
+// Whether the first `outs` ranges share a byte with each other or with a later one.
+template <int kN>
+bool any_overlap(const Range (&r)[kN], int outs)
+{
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < kN; ++j)
+            if (overlaps(r[i].p, r[i].n, r[j].p, r[j].n))
+                return true;
+    return false;
+}
+
+bool operand_ok(int32_t o) { return o == HKG_MX_OPERAND_A || o == HKG_MX_OPERAND_B; }
+
+int quantize(int32_t operand, int32_t operand_t, int64_t rows, int64_t K, const void *x,
+             int32_t x_type, int64_t ldx, void *codes, void *packed, void *codes_t, void *packed_t,
+             bool both, void *stream)
+{
+    const int64_t e = elem_size(x_type);
+    if (!operand_ok(operand) || !operand_ok(operand_t) || !e)
+        return HKG_ERR_OPTS;
+    if (rows < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (rows == 0 || K == 0)
+        return HKG_OK;
+    if (!x || !codes || !packed || (both && (!codes_t || !packed_t)))
+        return HKG_ERR_NULL;
+    int rc = check_matrix(x, rows, K, e, &ldx);
+    if (rc != HKG_OK)
+        return rc;
+    if (!aligned16(codes) || !aligned16(packed) || !aligned16(codes_t) || !aligned16(packed_t))
+        return HKG_ERR_ALIGN;
+    if (!mx4_fits(rows, K) || (both && !mx4_fits(K, rows)))
+        return HKG_ERR_SIZE;
+    const Range r[] = {{codes, mx4_codes(rows, K)},
+                       {packed, mx4_scales(rows, K)},
+                       {both ? codes_t : nullptr, mx4_codes(K, rows)},
+                       {both ? packed_t : nullptr, mx4_scales(K, rows)},
+                       {x, extent(rows, K, ldx, e)}};
+    if (any_overlap(r, 4))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+    const hkg::QuantParams p = {x, ldx, static_cast<int>(rows), static_cast<int>(K), operand, operand_t,
+                                static_cast<uint8_t *>(codes), static_cast<uint8_t *>(packed),
+                                both ? static_cast<uint8_t *>(codes_t) : nullptr,
+                                both ? static_cast<uint8_t *>(packed_t) : nullptr};
+    return launched(hkg::launch_mx4_quantize(x_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16, p,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+// Shape and operand checks of one product; a pointer may be null where its
+// matrix is empty.
+int check_product(int64_t M, int64_t N, int64_t K, const void *B, const void *SB, const void *C,
+                  int64_t *ldc)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (M == 0 || N == 0)
+        return HKG_OK;
+    if (!C || (K > 0 && (!B || !SB)))
+        return HKG_ERR_NULL;
+    int rc = check_matrix(C, M, N, 2, ldc);
+    if (rc != HKG_OK)
+        return rc;
+    if (!aligned16(B) || !aligned16(SB) || !aligned16(C))
+        return HKG_ERR_ALIGN;
+    if (!mx4_fits(M, K) || !mx4_fits(N, K) ||
+        ceil_div(M, kTile) * ceil_div(N, kTile) >= (int64_t(1) << 30))
+        return HKG_ERR_SIZE;
+    return HKG_OK;
+}
+
+hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const void *SA,
+                           const void *B, const void *SB, void *C, float *C_f32, int64_t ldc)
+{
+    hkg::Mx4GemmParams p = {};
+    p.A = static_cast<const uint8_t *>(A);
+    p.SA = static_cast<const uint8_t *>(SA);
+    p.B = static_cast<const uint8_t *>(B);
+    p.SB = static_cast<const uint8_t *>(SB);
+    p.C = static_cast<uint16_t *>(C);
+    p.C_f32 = C_f32;
+    p.ldc = ldc;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.kb = static_cast<int>(pad32(K) / 2);
+    return p;
+}
+
+hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
+{
+    return hkg::launch_mx4_direct(hkg::kElemBf16, p, static_cast<hipStream_t>(stream));
+}
+
+// Rows of x up to which the linear layer quantises inside the product.
+constexpr int64_t kFusedRows = 16;
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+}  // namespace hkg::api
+
+using namespace hkg::api;
+
+extern "C" {
+
+int64_t hkg_mxfp4_code_bytes(int64_t rows, int64_t K)
+{
+    if (rows < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (!mx4_fits(rows, K))
+        return HKG_ERR_SIZE;
+    return mx4_codes(rows, K);
+}
+
+int hkg_mxfp4_quantize(int32_t operand, int64_t rows, int64_t K, const void *x, int32_t x_type,
+                       int64_t ldx, void *codes, void *packed, void *stream)
+{
+    return quantize(operand, operand, rows, K, x, x_type, ldx, codes, packed, nullptr, nullptr, false,
+                    stream);
+}
+
+int hkg_mxfp4_quantize_both(int32_t operand, int32_t operand_t, int64_t rows, int64_t K,
+                            const void *x, int32_t x_type, int64_t ldx, void *codes, void *packed,
+                            void *codes_t, void *packed_t, void *stream)
+{
+    return quantize(operand, operand_t, rows, K, x, x_type, ldx, codes, packed, codes_t, packed_t,
+                    true, stream);
+}
+
+int hkg_mxfp4_dequantize(int32_t operand, int64_t rows, int64_t K, const void *codes,
+                         const void *packed, void *values, int32_t v_type, int64_t ldv,
+                         void *stream)
+{
+    const int64_t e = elem_size(v_type);
+    if (!operand_ok(operand) || !e)
+        return HKG_ERR_OPTS;
+    if (rows < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (rows == 0 || K == 0)
+        return HKG_OK;
+    if (!codes || !packed || !values)
+        return HKG_ERR_NULL;
+    if (!mx4_fits(rows, K))
+        return HKG_ERR_SIZE;
+    const int64_t kp = pad32(K);
+    int rc = check_matrix(values, rows, kp, e, &ldv);
+    if (rc != HKG_OK)
+        return rc;
+    if (!aligned16(codes) || !aligned16(packed))
+        return HKG_ERR_ALIGN;
+    const Range r[] = {{values, extent(rows, kp, ldv, e)},
+                       {codes, mx4_codes(rows, K)},
+                       {packed, mx4_scales(rows, K)}};
+    if (any_overlap(r, 1))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+    const hkg::DequantParams p = {static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(packed),
+                                  values, ldv, static_cast<int>(rows), static_cast<int>(kp), operand};
+    return launched(hkg::launch_mx4_dequantize(v_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16, p,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int hkg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, const void *B, const void *SA,
+                   const void *SB, void *C, float *C_f32, int64_t ldc, void *stream)
+{
+    int rc = check_product(M, N, K, B, SB, C, &ldc);
+    if (rc != HKG_OK || M == 0 || N == 0)
+        return rc;
+    if (K > 0 && (!A || !SA))
+        return HKG_ERR_NULL;
+    if (!aligned16(A) || !aligned16(SA) || !aligned16(C_f32))
+        return HKG_ERR_ALIGN;
+    const Range r[] = {{C, extent(M, N, ldc, 2)}, {C_f32, extent(M, N, ldc, 4)},
+                       {A, mx4_codes(M, K)},      {SA, mx4_scales(M, K)},
+                       {B, mx4_codes(N, K)},      {SB, mx4_scales(N, K)}};
+    if (any_overlap(r, 2))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+    return launched(run_product(product(M, N, K, A, SA, B, SB, C, C_f32, ldc), stream));
+}
+
+int64_t hkg_linear_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (!mx4_fits(M, K) || !mx4_fits(N, K))
+        return HKG_ERR_SIZE;
+    return M <= kFusedRows || N == 0 ? 0 : round16(mx4_codes(M, K)) + mx4_scales(M, K);
+}
+
+int hkg_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void *x, int32_t x_type, int64_t ldx,
+                     const void *W, const void *SW, void *y, int64_t ldy, void *workspace,
+                     int64_t workspace_bytes, void *stream)
+{
+    const int64_t e = elem_size(x_type);
+    if (!e)
+        return HKG_ERR_OPTS;
+    int rc = check_product(M, N, K, W, SW, y, &ldy);
+    if (rc != HKG_OK || M == 0 || N == 0)
+        return rc;
+    if (K > 0) {
+        if (!x)
+            return HKG_ERR_NULL;
+        rc = check_matrix(x, M, K, e, &ldx);
+        if (rc != HKG_OK)
+            return rc;
+    }
+    const int64_t need = hkg_linear_mxfp4_workspace_bytes(M, N, K);
+    if (need > 0) {
+        if (!workspace)
+            return HKG_ERR_NULL;
+        if (!aligned16(workspace))
+            return HKG_ERR_ALIGN;
+        if (workspace_bytes < need)
+            return HKG_ERR_WORKSPACE;
+    }
+    const Range r[] = {{y, extent(M, N, ldy, 2)},
+                       {need > 0 ? workspace : nullptr, need},
+                       {x, extent(M, K, ldx, e)},
+                       {W, mx4_codes(N, K)},
+                       {SW, mx4_scales(N, K)}};
+    if (any_overlap(r, 2))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+    const hkg::ElemType t = x_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (need == 0) {
+        hkg::Mx4GemmParams p = product(M, N, K, nullptr, nullptr, W, SW, y, nullptr, ldy);
+        p.x = x;
+        p.ldx = ldx;
+        return launched(hkg::launch_mx4_direct(t, p, st));
+    }
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *packed = codes + round16(mx4_codes(M, K));
+    const hkg::QuantParams q = {x, ldx, static_cast<int>(M), static_cast<int>(K), HKG_MX_OPERAND_A,
+                                HKG_MX_OPERAND_A, codes, packed, nullptr, nullptr};
+    rc = K > 0 ? launched(hkg::launch_mx4_quantize(t, q, st)) : HKG_OK;
+    if (rc != HKG_OK)
+        return rc;
+    return launched(run_product(product(M, N, K, codes, packed, W, SW, y, nullptr, ldy), stream));
+}
+
+int64_t hkg_linear_mxfp4_backward_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    if (!mx4_fits(M, N) || !mx4_fits(N, M) || !mx4_fits(K, N) || !mx4_fits(K, M))
+        return HKG_ERR_SIZE;
+    return round16(mx4_codes(M, N)) + mx4_scales(M, N) + round16(mx4_codes(N, M)) + mx4_scales(N, M);
+}
+
+int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, int32_t dy_type,
+                              int64_t lddy, const void *Wt, const void *SWt, const void *Xt,
+                              const void *SXt, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                              void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int64_t e = elem_size(dy_type);
+    if (!e)
+        return HKG_ERR_OPTS;
+    if (M < 0 || N < 0 || K < 0)
+        return HKG_ERR_SHAPE;
+    const bool want_x = dx && M > 0 && K > 0, want_w = dw && N > 0 && K > 0;
+    if (!want_x && !want_w)
+        return HKG_OK;
+    int rc = want_x ? check_product(M, K, N, Wt, SWt, dx, &lddx) : HKG_OK;
+    if (rc == HKG_OK && want_w)
+        rc = check_product(N, K, M, Xt, SXt, dw, &lddw);
+    if (rc != HKG_OK)
+        return rc;
+    const bool have = M > 0 && N > 0;
+    const int64_t need = hkg_linear_mxfp4_backward_workspace_bytes(M, N, K);
+    if (need < 0)
+        return static_cast<int>(need);
+    if (have) {
+        if (!dy || !workspace)
+            return HKG_ERR_NULL;
+        rc = check_matrix(dy, M, N, e, &lddy);
+        if (rc != HKG_OK)
+            return rc;
+        if (!aligned16(workspace))
+            return HKG_ERR_ALIGN;
+        if (workspace_bytes < need)
+            return HKG_ERR_WORKSPACE;
+    }
+    const Range r[] = {{want_x ? dx : nullptr, extent(M, K, lddx, 2)},
+                       {want_w ? dw : nullptr, extent(N, K, lddw, 2)},
+                       {have ? workspace : nullptr, need},
+                       {dy, extent(M, N, lddy, e)},
+                       {want_x ? Wt : nullptr, mx4_codes(K, N)},
+                       {want_x ? SWt : nullptr, mx4_scales(K, N)},
+                       {want_w ? Xt : nullptr, mx4_codes(K, M)},
+                       {want_w ? SXt : nullptr, mx4_scales(K, M)}};
+    if (any_overlap(r, 3))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t *q = static_cast<uint8_t *>(workspace), *s = q + round16(mx4_codes(M, N)),
+            *qt = s + mx4_scales(M, N), *stt = qt + round16(mx4_codes(N, M));
+    if (have) {
+        const hkg::QuantParams p = {dy, lddy, static_cast<int>(M), static_cast<int>(N), HKG_MX_OPERAND_A,
+                                    HKG_MX_OPERAND_A, q, s, want_w ? qt : nullptr, want_w ? stt : nullptr};
+        rc = launched(hkg::launch_mx4_quantize(dy_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16, p, st));
+    }
+    if (rc == HKG_OK && want_x)
+        rc = launched(run_product(product(M, K, N, q, s, Wt, SWt, dx, nullptr, lddx), stream));
+    if (rc == HKG_OK && want_w)
+        rc = launched(run_product(product(N, K, M, qt, stt, Xt, SXt, dw, nullptr, lddw), stream));
+    return rc;
+}
+
+}  // extern "C"

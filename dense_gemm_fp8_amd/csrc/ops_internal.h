@@ -1,0 +1,57 @@
+// ops_internal.h -- host checks shared by the entry points of hkg_ops.h
+// (ops_api.cpp, orth_api.cpp) and those of hkg.h (hkg_api.cpp, which defines
+// the ones declared here without a body).  Not part of the installed interface.
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/hkg_ops.h"
+#include "api_internal.h"
+
+namespace hkg::api {
+
+bool mx_sizes_fit(int64_t rows, int64_t K);
+bool aligned16(const void *p);
+int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t elem);
+bool overlaps(const void *p, int64_t pb, const void *q, int64_t qb);
+
+inline int64_t pad32(int64_t K) { return (K + 31) / 32 * 32; }
+
+// An MXFP4 matrix [rows][K] within the limits; K is compared before it is
+// rounded up, so no value can wrap.
+inline bool mx4_fits(int64_t rows, int64_t K)
+{
+    return K < (int64_t(1) << 23) - 32 && mx_sizes_fit(rows, pad32(K));
+}
+inline int64_t mx4_codes(int64_t rows, int64_t K) { return rows * (pad32(K) / 2); }
+inline int64_t mx4_scales(int64_t rows, int64_t K) { return mx_packed_bytes(rows, pad32(K)); }
+
+// Element size of an HKG_T_* value, 0 if it is none.
+inline int64_t elem_size(int32_t t) { return t == HKG_T_BF16 ? 2 : t == HKG_T_F32 ? 4 : 0; }
+
+// A matrix [rows][cols] of elements with pitch *ld (0 becomes cols): pitch at
+// least the row (HKG_ERR_OPTS), base aligned to its element (HKG_ERR_ALIGN),
+// extents that cannot wrap (HKG_ERR_SIZE).
+inline int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t elem, int64_t *ld)
+{
+    if (*ld == 0)
+        *ld = cols;
+    if (*ld < cols)
+        return HKG_ERR_OPTS;
+    if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elem))
+        return HKG_ERR_ALIGN;
+    if (rows >= (int64_t(1) << 31) || *ld >= (int64_t(1) << 31))
+        return HKG_ERR_SIZE;
+    return HKG_OK;
+}
+
+// Record a launch's HIP error, if it has one, as the entry points of hkg.h do.
+inline int launched(hipError_t e)
+{
+    if (e == hipSuccess)
+        return HKG_OK;
+    set_last_hip_error(static_cast<int>(e));
+    return HKG_ERR_LAUNCH;
+}
+
+}  // namespace hkg::api

@@ -1,0 +1,47 @@
+// ops_kernels.h -- launch interface between the operators' entry points
+// (ops_api.cpp) and their gfx950 kernels (mxfp4_kernels.hip).  Internal to
+// libhkg; all argument checks are done by the caller.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hkg {
+
+enum ElemType { kElemBf16 = 0, kElemF32 = 1 };
+
+// One quantisation pass over x [rows][K] (rows ldx elements apart).  codes_t
+// null: along K only.
+struct QuantParams {
+    const void *x;
+    int64_t ldx;
+    int rows, K;
+    int operand, operand_t;
+    uint8_t *codes, *packed;       // [rows][Kp/2], packed scales
+    uint8_t *codes_t, *packed_t;   // [K][Rp/2], packed scales of the transposed form
+};
+hipError_t launch_mx4_quantize(ElemType t, const QuantParams &p, hipStream_t stream);
+
+struct DequantParams {
+    const uint8_t *codes, *packed;
+    void *values;
+    int64_t ldv;
+    int rows, kp;                  // kp: K rounded up to 32
+    int operand;
+};
+hipError_t launch_mx4_dequantize(ElemType t, const DequantParams &p, hipStream_t stream);
+
+// C[M][N] = A B^T of MXFP4 operands, kb = bytes of an operand row (Kp / 2).
+struct Mx4GemmParams {
+    const uint8_t *A, *B;          // codes; A null: quantise x inside the product
+    const uint8_t *SA, *SB;        // packed scales
+    const void *x;                 // [M][K] values (A null)
+    int64_t ldx;
+    uint16_t *C;                   // bf16
+    float *C_f32;                  // or null
+    int64_t ldc;
+    int M, N, K, kb;
+};
+hipError_t launch_mx4_direct(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
+
+}  // namespace hkg

@@ -1,0 +1,259 @@
+"""Python binding of include/hkg_ops.h: the MXFP4 linear layer on GPU
+tensors.
+
+An MXFP4 matrix is a pair (codes, packed): uint8 [rows, Kp / 2] with two e2m1
+codes a byte (Kp = K rounded up to 32) and its E8M0 scales in packed order.
+
+    w, sw, wt, swt = mxfp4_quantize_both(W, B, B)        # once per weight update
+    x, sx, xt, sxt = mxfp4_quantize_both(X, A, B)        # a training step's input
+    y = gemm_mxfp4(x, w, sx, sw)                         # its forward product
+    dx, dw = linear_mxfp4_backward(dy, wt, swt, xt, sxt)
+    y = linear_mxfp4(X, w, sw)                           # serving, from one row up
+
+with A, B = HKG_MX_OPERAND_A, HKG_MX_OPERAND_B.  Every function takes `stream`
+(default: torch's current one) and enqueues its work there; outputs and
+workspaces it allocates belong to that stream.  A failed check raises
+HkgError with the library's status (ValueError / TypeError for tensors of the
+wrong kind); nothing has run then.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import dense_gemm_fp8_amd as _hkg
+
+HKG_T_BF16 = 0
+HKG_T_F32 = 1
+
+# exported symbols, in the order include/hkg_ops.h declares them
+OPS_EXPORTS = (
+    "hkg_mxfp4_code_bytes",
+    "hkg_mxfp4_quantize",
+    "hkg_mxfp4_quantize_both",
+    "hkg_mxfp4_dequantize",
+    "hkg_gemm_mxfp4",
+    "hkg_linear_mxfp4_workspace_bytes",
+    "hkg_linear_mxfp4",
+    "hkg_linear_mxfp4_backward_workspace_bytes",
+    "hkg_linear_mxfp4_backward",
+)
+
+_ready = None
+
+
+def _lib() -> ctypes.CDLL:
+    """libhkg with the argument types of hkg_ops.h set."""
+    global _ready
+    if _ready is None:
+        lib = _hkg.load()
+        i64, i32, p, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+        sig = {
+            "hkg_mxfp4_code_bytes": [i64, i64],
+            "hkg_mxfp4_quantize": [i32, i64, i64, p, i32, i64, p, p, p],
+            "hkg_mxfp4_quantize_both": [i32, i32, i64, i64, p, i32, i64, p, p, p, p, p],
+            "hkg_mxfp4_dequantize": [i32, i64, i64, p, p, p, i32, i64, p],
+            "hkg_gemm_mxfp4": [i64, i64, i64, p, p, p, p, p, p, i64, p],
+            "hkg_linear_mxfp4_workspace_bytes": [i64, i64, i64],
+            "hkg_linear_mxfp4": [i64, i64, i64, p, i32, i64, p, p, p, i64, p, i64, p],
+            "hkg_linear_mxfp4_backward_workspace_bytes": [i64, i64, i64],
+            "hkg_linear_mxfp4_backward": [i64, i64, i64, p, i32, i64, p, p, p, p, p, i64, p, i64, p,
+                                          i64, p],
+        }
+        for name, args in sig.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = i64 if name.endswith("_bytes") else ctypes.c_int
+        _ready = lib
+    return _ready
+
+
+def _check(rc, name):
+    if rc < 0:
+        raise _hkg.HkgError(rc, name)
+    return rc
+
+
+def _pad32(k: int) -> int:
+    return -(-k // 32) * 32
+
+
+def _elem_type(t, name) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return HKG_T_BF16
+    if t.dtype == torch.float32:
+        return HKG_T_F32
+    raise TypeError("%s must be bfloat16 or float32" % name)
+
+
+def _codes(t, rows, K, name):
+    """Pointer of the codes of a [rows, K] MXFP4 matrix (K None: any)."""
+    import torch
+    if t.dtype != torch.uint8 or t.dim() != 2:
+        raise TypeError("%s must be a 2-D uint8 tensor of e2m1 codes" % name)
+    if t.shape[0] != rows or t.shape[1] != _pad32(K) // 2:
+        raise ValueError("%s must be [%d, %d]" % (name, rows, _pad32(K) // 2))
+    return _hkg._dev_ptr(t, name)
+
+
+def _packed(t, rows, K, name):
+    import torch
+    need = _hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K))
+    if t.dtype != torch.uint8 or (need >= 0 and t.numel() < need):
+        raise ValueError("%s must be a uint8 tensor of at least %d bytes" % (name, need))
+    return _hkg._dev_ptr(t, name)
+
+
+class _On:
+    """The stream a call runs on: its handle, and allocations that belong to it
+    (a block freed while the stream still uses it is then reused in its order)."""
+
+    def __init__(self, stream, device):
+        import torch
+        self._torch, self._device = torch, device
+        self._stream = stream
+        self.handle = _hkg._stream_handle(stream)
+
+    def empty(self, shape, dtype):
+        ctx = self._torch.cuda.stream(self._stream) if self._stream is not None else contextlib.nullcontext()
+        with ctx:
+            return self._torch.empty(shape, dtype=dtype, device=self._device)
+
+    def bytes(self, n):
+        return self.empty((max(int(n), 16),), self._torch.uint8)
+
+
+def _output(on, t, shape, dtype, name):
+    """t, or a new tensor; -> (tensor, pointer, row pitch)."""
+    if t is None:
+        t = on.empty(shape, dtype)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError("%s must be a %s tensor of shape %s" % (name, dtype, tuple(shape)))
+    ptr, ld = _hkg._matrix(t, name)
+    return t, ptr, ld
+
+
+def _workspace(on, t, need, name):
+    """Pointer and size of the caller's workspace, or of a new one."""
+    if need <= 0:
+        return None, None, 0
+    if t is None:
+        t = on.bytes(need)
+    return t, _hkg._dev_ptr(t, name), t.numel() * t.element_size()
+
+
+def mxfp4_quantize(x, operand, stream=None):
+    """MXFP4 form of x [rows, K] (bf16 or fp32, rows contiguous) along K ->
+    (codes [rows, Kp / 2], packed scales for `operand`)."""
+    import torch
+    xt = _elem_type(x, "x")
+    px, ld = _hkg._matrix(x, "x")
+    rows, K = x.shape
+    on = _On(stream, x.device)
+    _check(_lib().hkg_mxfp4_code_bytes(rows, K), "hkg_mxfp4_code_bytes")
+    codes = on.empty((rows, _pad32(K) // 2), torch.uint8)
+    packed = on.bytes(_hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K)))
+    _check(_lib().hkg_mxfp4_quantize(operand, rows, K, px, xt, ld, codes.data_ptr(), packed.data_ptr(),
+                                     on.handle), "hkg_mxfp4_quantize")
+    return codes, packed
+
+
+def mxfp4_quantize_both(x, operand, operand_t, stream=None):
+    """mxfp4_quantize(x) and, from the same pass over x, the MXFP4 form of x^T
+    -> (codes, packed, codes_t [K, Rp / 2], packed_t)."""
+    import torch
+    xt = _elem_type(x, "x")
+    px, ld = _hkg._matrix(x, "x")
+    rows, K = x.shape
+    on = _On(stream, x.device)
+    _check(_lib().hkg_mxfp4_code_bytes(rows, K), "hkg_mxfp4_code_bytes")
+    _check(_lib().hkg_mxfp4_code_bytes(K, rows), "hkg_mxfp4_code_bytes")
+    codes = on.empty((rows, _pad32(K) // 2), torch.uint8)
+    codes_t = on.empty((K, _pad32(rows) // 2), torch.uint8)
+    packed = on.bytes(_hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K)))
+    packed_t = on.bytes(_hkg.hkg_mx_packed_scale_bytes(K, _pad32(rows)))
+    _check(_lib().hkg_mxfp4_quantize_both(operand, operand_t, rows, K, px, xt, ld, codes.data_ptr(),
+                                          packed.data_ptr(), codes_t.data_ptr(), packed_t.data_ptr(),
+                                          on.handle), "hkg_mxfp4_quantize_both")
+    return codes, packed, codes_t, packed_t
+
+
+def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
+    """The values of an MXFP4 matrix, [rows, Kp] in bf16 (default) or fp32."""
+    import torch
+    if codes.dim() != 2:
+        raise TypeError("codes must be a 2-D uint8 tensor of e2m1 codes")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if K % 32:
+        raise ValueError("codes must hold whole blocks of 32 (16 bytes a row)")
+    pc, pp = _codes(codes, rows, K, "codes"), _packed(packed, rows, K, "packed")
+    on = _On(stream, codes.device)
+    dtype = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
+    out, po, ld = _output(on, out, (rows, K), dtype, "out")
+    _check(_lib().hkg_mxfp4_dequantize(operand, rows, K, pc, pp, po, _elem_type(out, "out"), ld,
+                                       on.handle), "hkg_mxfp4_dequantize")
+    return out
+
+
+def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
+    """C[M,N] (bf16) = A[M,K] · B[N,K]ᵀ of two MXFP4 matrices; returns C."""
+    import torch
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError("A is [M,K/2] and B is [N,K/2]")
+    M, N, K = A.shape[0], B.shape[0], 2 * A.shape[1]
+    if K % 32:
+        raise ValueError("A and B must hold whole blocks of 32 (16 bytes a row)")
+    pa, pb = _codes(A, M, K, "A"), _codes(B, N, K, "B")
+    sa, sb = _packed(SA_packed, M, K, "SA_packed"), _packed(SB_packed, N, K, "SB_packed")
+    on = _On(stream, A.device)
+    C, pc, ldc = _output(on, C, (M, N), torch.bfloat16, "C")
+    pf = None
+    if C_f32 is not None:
+        C_f32, pf, ldf = _output(on, C_f32, (M, N), torch.float32, "C_f32")
+        if ldf != ldc:
+            raise ValueError("C and C_f32 must have the same row pitch")
+    _check(_lib().hkg_gemm_mxfp4(M, N, K, pa, pb, sa, sb, pc, pf, ldc, on.handle), "hkg_gemm_mxfp4")
+    return C
+
+
+def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
+    """y[M,N] (bf16) = Q(x)[M,K] · W[N,K]ᵀ with x quantised to MXFP4 on the way
+    (x bf16 or fp32; W, SW_packed an MXFP4 matrix packed for operand B).
+    workspace: a uint8 tensor of hkg_linear_mxfp4_workspace_bytes(M, N, K)."""
+    import torch
+    xt = _elem_type(x, "x")
+    px, ldx = _hkg._matrix(x, "x")
+    M, K = x.shape
+    N = W.shape[0]
+    pw, ps = _codes(W, N, K, "W"), _packed(SW_packed, N, K, "SW_packed")
+    on = _On(stream, x.device)
+    y, py, ldy = _output(on, y, (M, N), torch.bfloat16, "y")
+    need = _check(_lib().hkg_linear_mxfp4_workspace_bytes(M, N, K), "hkg_linear_mxfp4_workspace_bytes")
+    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
+    _check(_lib().hkg_linear_mxfp4(M, N, K, px, xt, ldx, pw, ps, py, ldy, pws, nws, on.handle),
+           "hkg_linear_mxfp4")
+    return y
+
+
+def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, workspace=None,
+                          stream=None):
+    """Gradients of y = Q(x) Wᵀ, rounding passed straight through: (dx [M,K], dw
+    [N,K]) in bf16 from dy [M,N] (bf16 or fp32) and the MXFP4 forms of Wᵀ [K,N]
+    and xᵀ [K,M] packed for operand B (mxfp4_quantize_both)."""
+    import torch
+    t = _elem_type(dy, "dy")
+    pdy, lddy = _hkg._matrix(dy, "dy")
+    M, N = dy.shape
+    K = Wt.shape[0]
+    pw, psw = _codes(Wt, K, N, "Wt"), _packed(SWt_packed, K, N, "SWt_packed")
+    px, psx = _codes(Xt, K, M, "Xt"), _packed(SXt_packed, K, M, "SXt_packed")
+    on = _On(stream, dy.device)
+    dx, pdx, lddx = _output(on, dx, (M, K), torch.bfloat16, "dx")
+    dw, pdw, lddw = _output(on, dw, (N, K), torch.bfloat16, "dw")
+    need = _check(_lib().hkg_linear_mxfp4_backward_workspace_bytes(M, N, K),
+                  "hkg_linear_mxfp4_backward_workspace_bytes")
+    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
+    _check(_lib().hkg_linear_mxfp4_backward(M, N, K, pdy, t, lddy, pw, psw, px, psx, pdx, lddx, pdw,
+                                            lddw, pws, nws, on.handle), "hkg_linear_mxfp4_backward")
+    return dx, dw

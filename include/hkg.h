@@ -67,8 +67,9 @@ typedef enum {
     HKG_ERR_LAUNCH = -7,  /* a kernel launch failed; see hkg_last_hip_error().  When
                              the call was split into two launches (hkg_launch_plan),
                              the rows of the first may already be written         */
-    HKG_ERR_OVERLAP = -8  /* C or C_f32 shares bytes with A, B, the packed MXFP8
+    HKG_ERR_OVERLAP = -8, /* C or C_f32 shares bytes with A, B, the packed MXFP8
                              scales or the other output (A and B may alias)          */
+    HKG_ERR_WORKSPACE = -9/* a workspace (hkg_ops.h) is smaller than the call needs  */
 } hkg_status;
 
 /* Grid order (the remap of the HipKittens L2 note, section 2 Pillar 3 / section 7 Algorithm 1). */
