@@ -106,9 +106,19 @@ hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const
     return p;
 }
 
+// Grid order of a tile grid: as the GEMM of hkg.h, whose rows of kb bytes these are.
+hkg::TileOrder order_of(int64_t M, int64_t N, int64_t row_bytes, int tile)
+{
+    const bool big = row_bytes > 18944;
+    int64_t Gm = ceil_div(M, tile), Gn = ceil_div(N, tile), w = big ? 16 : 8, c = big ? 4 : 32;
+    clamp_remap(Gm, Gn, &w, &c);
+    return {static_cast<int>(Gm), static_cast<int>(Gn), static_cast<int>(w), static_cast<int>(c)};
+}
+
 hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 {
-    return hkg::launch_mx4_direct(hkg::kElemBf16, p, static_cast<hipStream_t>(stream));
+    const int tile = ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128 ? 128 : 256;
+    return hkg::launch_mx4_tiles(tile, order_of(p.M, p.N, p.kb, tile), p, static_cast<hipStream_t>(stream));
 }
 
 // Rows of x up to which the linear layer quantises inside the product.

@@ -1,5 +1,5 @@
 // ops_kernels.h -- launch interface between the operators' entry points
-// (ops_api.cpp) and their gfx950 kernels (mxfp4_kernels.hip).  Internal to
+// (ops_api.cpp) and their gfx950 kernels (mxfp4_kernels.hip, mxfp4_gemm.hip).  Internal to
 // libhkg; all argument checks are done by the caller.
 #pragma once
 
@@ -43,5 +43,12 @@ struct Mx4GemmParams {
     int M, N, K, kb;
 };
 hipError_t launch_mx4_direct(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
+
+// A grid of Gm x Gn tiles and the order its workgroups walk it in (remap.h).
+struct TileOrder {
+    int Gm, Gn, W, C;
+};
+// The same product on tile x tile output tiles (256 or 128); A is codes.
+hipError_t launch_mx4_tiles(int tile, const TileOrder &order, const Mx4GemmParams &p, hipStream_t stream);
 
 }  // namespace hkg
