@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const 
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
     settle(acc);
-    store_bf16<kT>(p, tm, tn, loop.a_rows / kStepBytes, (loop.b_rows - Loop::kRingB) / kStepBytes, loop.lane, acc);
+    store_bf16<kT>(p, tm, tn, loop.a_rows / kStepBytes, loop.b_rows / kStepBytes, loop.lane, acc);
 }
 
 }  // namespace

@@ -79,6 +79,12 @@ __device__ __forceinline__ int hold_s(int x)
     asm volatile("" : "+s"(x));
     return x;
 }
+__device__ __forceinline__ uint32_t copy_v(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("v_mov_b32 %0, %1" : "=v"(y) : "v"(x));
+    return y;
+}
 __device__ __forceinline__ int copy_s(int x)
 {
     int y;
@@ -193,7 +199,8 @@ struct TileLoop {
     __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
     char *smem;
     int wave, lane;
-    int a_rows, b_rows;            // LDS bytes of the wave's rows in panel 0
+    int w_load;                    // LDS bytes of its first row group in a panel
+    int a_rows, b_rows;            // LDS bytes of its rows in a panel
     int voff_a, voff_b;            // lane's load offset: its row and permuted chunk
     int cb_a, cb_b;                // byte of that chunk in a K step
     int pitch_a, pitch_b, kb;
@@ -208,8 +215,9 @@ struct TileLoop {
         smem = lds;
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        w_load = wave * kLoadBytes;
         a_rows = (kT / 2) * (wave >> 1) * kStepBytes;
-        b_rows = kRingB + (kT / 2) * (wave & 1) * kStepBytes;
+        b_rows = (kT / 2) * (wave & 1) * kStepBytes;
         pitch_a = p.pitch_a;
         pitch_b = p.pitch_b;
         kb = p.kb;
@@ -221,8 +229,8 @@ struct TileLoop {
         const int r8 = lane >> 3;
         cb_a = ((lane & 7) ^ swz_a(r8 | (wave << 3))) << 4;
         cb_b = ((lane & 7) ^ swz_b(r8 | (wave << 3))) << 4;
-        voff_a = r8 * pitch_a + cb_a;
-        voff_b = r8 * pitch_b + cb_b;
+        voff_a = (8 * wave + r8) * pitch_a + cb_a;
+        voff_b = (8 * wave + r8) * pitch_b + cb_b;
         const int x = lane & 15, q = lane >> 4, xb = (x & 3) + 8 * (x >> 2);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -245,12 +253,14 @@ struct TileLoop {
         }
     }
 
-    __device__ __forceinline__ void load8rows(__amdgpu_buffer_rsrc_t rs, int lds_off, int u, int voff, int soff,
+    // Rows 8 (wave + 4 v) .. + 7 of a panel; lds_off: the panel's place in its
+    // ring, counted from the wave's first row group.
+    __device__ __forceinline__ void load8rows(__amdgpu_buffer_rsrc_t rs, int lds_off, int v, int voff, int soff,
                                               int pitch) const
     {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void *)(smem + lds_off + u * kLoadBytes), 16, voff,
-            soff + u * 8 * pitch, 0, 0);
+            rs, (__attribute__((address_space(3))) void *)(smem + lds_off + 4 * v * kLoadBytes), 16, voff,
+            soff + 32 * v * pitch, 0, 0);
     }
     // Lane offset in a K step that starts `at` bytes into the rows: a chunk past
     // the rows' end reads zeros (kb is whole chunks).
@@ -313,6 +323,7 @@ struct TileLoop {
 
     __device__ __forceinline__ void run(f32x4_t (&acc)[kB][kB], int nk)
     {
+        constexpr int kHi = kB == 8;             // the last scale word
         constexpr bool kMasked = Mma::kScaled;   // fp16 operands come padded to whole K steps
         StepScales<kB> sc = {};
         if constexpr (Mma::kScaled)
@@ -324,16 +335,16 @@ struct TileLoop {
             const int vb = kMasked ? masked(voff_b, cb_b, s * kStepBytes) : voff_b;
 #pragma unroll
             for (int v = 0; v < kB; ++v)
-                load8rows(ra, s * kPanel, wave + 4 * v, va, s * kStepBytes, pitch_a);
+                load8rows(ra, w_load + s * kPanel, v, va, s * kStepBytes, pitch_a);
 #pragma unroll
             for (int v = 0; v < kB; ++v)
-                load8rows(rb, kRingB + s * kPanel, wave + 4 * v, vb, s * kStepBytes, pitch_b);
+                load8rows(rb, w_load + kRingB + s * kPanel, v, vb, s * kStepBytes, pitch_b);
         }
         wait_loads<2 * kB>();
         barrier();
         Frags f;
         {
-            const int ba = hold_v(la[0] + a_rows), bb = hold_v(lb[0] + b_rows);
+            const int ba = hold_v(la[0] + a_rows), bb = hold_v(lb[0] + kRingB + b_rows);
 #pragma unroll
             for (int j = 0; j < kB; ++j)
                 f.b[0][j] = *reinterpret_cast<const u32x4_t *>(smem + blk_b(j) + bb);
@@ -341,36 +352,40 @@ struct TileLoop {
             for (int i = 0; i < kB; ++i)
                 f.a[0][i] = *reinterpret_cast<const u32x4_t *>(smem + blk_a(i) + ba);
         }
-        // LDS offsets of A(t), B(t), B(t+1), B(t+2); K bytes of step t+2
-        int pa = 0, pb = 0, pb1 = kPanel, pb2 = 2 * kPanel, so = 2 * kStepBytes;
+        // LDS offsets of the wave's first row group in A(t), A(t+1), B(t), B(t+1),
+        // B(t+2), and of its fragments' rows from there; K bytes of step t+2
+        int pa = w_load, pa1 = pa + kPanel, pb = w_load + kRingB, pb1 = pb + kPanel, pb2 = pb1 + kPanel;
+        const int fa = a_rows - w_load, fb = b_rows - w_load;
+        int so = 2 * kStepBytes;
         int s_next = 2 * kMxStepScales;              // scales of step t+1
         int vb = kMasked ? masked(voff_b, cb_b, so) : voff_b;
-        int ba0 = hold_v(la[1] + a_rows), bb0 = hold_v(lb[1] + b_rows);   // half 1 of step t
+        int ba0 = hold_v(la[1] + fa + pa), bb0 = hold_v(lb[1] + fb + pb);   // half 1 of step t
         for (int t = 0; t < nk; ++t) {
             StepScales<kB> next = {};
-            if constexpr (Mma::kScaled) {
-                s_next = hold_s(s_next);
-                scales(next, min(s_next, s_last), min(s_next + kMxStepScales, s_last));
-            }
             int va = voff_a, vb_next = voff_b, ba1 = 0, bb1 = 0;
-            int npa = 0, nso = 0, npb = 0, npb1 = 0, npb2 = 0;
+            int npa = 0, npa1 = 0, nso = 0, npb = 0, npb1 = 0, npb2 = 0;
             __builtin_amdgcn_sched_barrier(0);
             half<0>(
                 f, acc, sc, ba0, bb0,
                 [&](int v) {
                     pb2 = hold_s(pb2);
                     so = hold_s(so);
-                    load8rows(rb, kRingB + pb2, wave + 4 * v, vb, so, pitch_b);
+                    load8rows(rb, pb2, v, vb, so, pitch_b);
                 },
                 [&](auto slot) __attribute__((always_inline)) {
                     constexpr int n = decltype(slot)::value;
+                    if constexpr (Mma::kScaled && n == 0) {
+                        // ahead of B's loads, which the wait below leaves in flight
+                        s_next = hold_s(s_next);
+                        scales(next, min(s_next, s_last), min(s_next + kMxStepScales, s_last));
+                    }
                     if constexpr (n == Plan::kBaseA) {
-                        pa = hold_s(pa);
-                        ba1 = hold_v(la[0] + hold_s(a_rows + (pa ^ kPanel)));
+                        pa1 = hold_s(pa1);
+                        ba1 = hold_v(la[0] + hold_s(fa + pa1));
                     }
                     if constexpr (n == Plan::kBaseB) {
                         pb1 = hold_s(pb1);
-                        bb1 = hold_v(lb[0] + hold_s(b_rows + pb1));
+                        bb1 = hold_v(lb[0] + hold_s(fb + pb1));
                     }
                     if constexpr (kMasked && n == Plan::kMask) {
                         so = hold_s(so);
@@ -385,18 +400,32 @@ struct TileLoop {
                 [&](int v) {
                     pa = hold_s(pa);
                     so = hold_s(so);
-                    load8rows(ra, pa, wave + 4 * v, va, so, pitch_a);
+                    load8rows(ra, pa, v, va, so, pitch_a);
                 },
                 [&](auto slot) __attribute__((always_inline)) {
                     constexpr int n = decltype(slot)::value;
                     if constexpr (n == Plan::kBaseA) {
-                        pa = hold_s(pa);
-                        ba0 = hold_v(la[1] + hold_s(a_rows + (pa ^ kPanel)));
+                        pa1 = hold_s(pa1);
+                        ba0 = hold_v(la[1] + hold_s(fa + pa1));
                     }
                     if constexpr (n == Plan::kBaseB) {
                         pb1 = hold_s(pb1);
-                        bb0 = hold_v(lb[1] + hold_s(b_rows + pb1));
+                        bb0 = hold_v(lb[1] + hold_s(fb + pb1));
                     }
+                    // the next step's scales move over those no instruction needs any
+                    // more (half 0's, and half 1's of A blocks 0..3 after 32 of 64):
+                    // left to the compiler, the moves bunch at the loop's end and
+                    // push accumulators out of their registers
+                    if constexpr (Mma::kScaled && n == 5)
+                        sc.b[0][0] = copy_v(next.b[0][0]);
+                    if constexpr (Mma::kScaled && n == 8)
+                        sc.a[0][0] = copy_v(next.a[0][0]);
+                    if constexpr (Mma::kScaled && kB == 8 && n == 14)
+                        sc.b[0][kHi] = copy_v(next.b[0][kHi]);
+                    if constexpr (Mma::kScaled && kB == 8 && n == 17)
+                        sc.a[0][kHi] = copy_v(next.a[0][kHi]);
+                    if constexpr (Mma::kScaled && kB == 8 && n == 40)
+                        sc.a[1][0] = copy_v(next.a[1][0]);
                     if constexpr (n == Plan::kRing)
                         npb = copy_s(pb1);
                     if constexpr (n == Plan::kRing + 1)
@@ -408,20 +437,25 @@ struct TileLoop {
                         vb_next = hold_v(masked(voff_b, cb_b, hold_s(so + kStepBytes)));
                     }
                     if constexpr (n == Plan::kTail) {
-                        npa = hold_s(hold_s(pa) ^ kPanel);
+                        npa = copy_s(pa1);
+                        npa1 = copy_s(pa);
                         nso = hold_s(hold_s(so) + kStepBytes);
                         if constexpr (Mma::kScaled)
                             s_next = hold_s(hold_s(s_next) + 2 * kMxStepScales);
                     }
                 });
             pa = npa;
+            pa1 = npa1;
             so = nso;
             pb = npb;
             pb1 = npb1;
             pb2 = npb2;
             vb = vb_next;
-            if constexpr (Mma::kScaled)
-                sc = next;
+            if constexpr (Mma::kScaled) {
+                sc.b[1][0] = next.b[1][0];
+                sc.b[1][kHi] = next.b[1][kHi];
+                sc.a[1][kHi] = next.a[1][kHi];
+            }
         }
         wait_loads<0>();
     }
