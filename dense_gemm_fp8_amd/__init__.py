@@ -490,9 +490,9 @@ def probe_xcd(workgroups, full_lds=True, spin_cycles=0, stream=None):
     return out
 
 
-# ---- MXFP4 linear layer (include/hkg_ops.h) -------------------------------------------
+# ---- MXFP4 linear layer and orthogonalised update (include/hkg_ops.h) -----------------
 
 HKG_ERR_WORKSPACE = -9
 
 from .ops import (gemm_mxfp4, linear_mxfp4, linear_mxfp4_backward,  # noqa: E402,F401
-                  mxfp4_dequantize, mxfp4_quantize, mxfp4_quantize_both)
+                  mxfp4_dequantize, mxfp4_quantize, mxfp4_quantize_both, orthogonalize)

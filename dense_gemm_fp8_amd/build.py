@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libhkg.so")
 SOURCES = [os.path.join(CSRC, "gemm_kernels.hip"), os.path.join(CSRC, "hkg_api.cpp"),
            os.path.join(CSRC, "launch.cpp"), os.path.join(CSRC, "remap_model.cpp"),
            os.path.join(CSRC, "tune.cpp"), os.path.join(CSRC, "mxfp4_kernels.hip"),
-           os.path.join(CSRC, "mxfp4_gemm.hip"), os.path.join(CSRC, "ops_api.cpp")]
+           os.path.join(CSRC, "mxfp4_gemm.hip"), os.path.join(CSRC, "ops_api.cpp"),
+           os.path.join(CSRC, "orth_kernels.hip"), os.path.join(CSRC, "orth_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

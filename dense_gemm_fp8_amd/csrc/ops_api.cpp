@@ -10,22 +10,6 @@
 namespace hkg::api {
 namespace {
 
-struct Range {
-    const void *p;
-    int64_t n;
-};
-
-// Whether the first `outs` ranges share a byte with each other or with a later one.
-template <int kN>
-bool any_overlap(const Range (&r)[kN], int outs)
-{
-    for (int i = 0; i < outs; ++i)
-        for (int j = i + 1; j < kN; ++j)
-            if (overlaps(r[i].p, r[i].n, r[j].p, r[j].n))
-                return true;
-    return false;
-}
-
 bool operand_ok(int32_t o) { return o == HKG_MX_OPERAND_A || o == HKG_MX_OPERAND_B; }
 
 int quantize(int32_t operand, int32_t operand_t, int64_t rows, int64_t K, const void *x,
@@ -106,15 +90,6 @@ hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const
     return p;
 }
 
-// Grid order of a tile grid: as the GEMM of hkg.h, whose rows of kb bytes these are.
-hkg::TileOrder order_of(int64_t M, int64_t N, int64_t row_bytes, int tile)
-{
-    const bool big = row_bytes > 18944;
-    int64_t Gm = ceil_div(M, tile), Gn = ceil_div(N, tile), w = big ? 16 : 8, c = big ? 4 : 32;
-    clamp_remap(Gm, Gn, &w, &c);
-    return {static_cast<int>(Gm), static_cast<int>(Gn), static_cast<int>(w), static_cast<int>(c)};
-}
-
 hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 {
     const int tile = ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128 ? 128 : 256;
@@ -123,8 +98,6 @@ hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 
 // Rows of x up to which the linear layer quantises inside the product.
 constexpr int64_t kFusedRows = 16;
-
-int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace hkg::api

@@ -7,6 +7,7 @@
 
 #include "../../include/hkg_ops.h"
 #include "api_internal.h"
+#include "ops_kernels.h"
 
 namespace hkg::api {
 
@@ -43,6 +44,34 @@ inline int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t elem,
     if (rows >= (int64_t(1) << 31) || *ld >= (int64_t(1) << 31))
         return HKG_ERR_SIZE;
     return HKG_OK;
+}
+
+struct Range {
+    const void *p;
+    int64_t n;
+};
+
+// Whether the first `outs` ranges share a byte with each other or with a later one.
+template <int kN>
+bool any_overlap(const Range (&r)[kN], int outs)
+{
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < kN; ++j)
+            if (overlaps(r[i].p, r[i].n, r[j].p, r[j].n))
+                return true;
+    return false;
+}
+
+inline int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Grid order of a tile grid whose operand rows hold row_bytes: the rule of the
+// GEMM of hkg.h (launch.cpp), measured there on the same loop's tiles.
+inline hkg::TileOrder order_of(int64_t M, int64_t N, int64_t row_bytes, int tile)
+{
+    const bool big = row_bytes > 18944;
+    int64_t Gm = ceil_div(M, tile), Gn = ceil_div(N, tile), w = big ? 16 : 8, c = big ? 4 : 32;
+    clamp_remap(Gm, Gn, &w, &c);
+    return {static_cast<int>(Gm), static_cast<int>(Gn), static_cast<int>(w), static_cast<int>(c)};
 }
 
 // Record a launch's HIP error, if it has one, as the entry points of hkg.h do.

@@ -1,0 +1,176 @@
+// orth_api.cpp -- hkg_orthogonalize (hkg_ops.h): argument checks, workspace
+// layout and the launches of its steps.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ops_internal.h"
+#include "orth_kernels.h"
+
+namespace hkg::api {
+namespace {
+
+int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// Byte offsets in the workspace: X [m][np], two X^T [n][mp] (the third product
+// reads one while it writes the other), A and P [m][mp], the norm's partial sums.
+struct OrthLayout {
+    int64_t m, n, mp, np;
+    int64_t x, xt[2], a, p, sums, bytes;
+};
+OrthLayout layout(int64_t rows, int64_t cols)
+{
+    OrthLayout l;
+    l.m = rows < cols ? rows : cols;
+    l.n = rows < cols ? cols : rows;
+    l.mp = pad64(l.m);
+    l.np = pad64(l.n);
+    int64_t at = 0;
+    auto take = [&](int64_t elems) {
+        const int64_t here = at;
+        at += 2 * elems;         // rows of 128 bytes: every part stays aligned
+        return here;
+    };
+    l.x = take(l.m * l.np);
+    l.xt[0] = take(l.n * l.mp);
+    l.xt[1] = take(l.n * l.mp);
+    l.a = take(l.m * l.mp);
+    l.p = take(l.m * l.mp);
+    l.sums = at;
+    l.bytes = at + round16(8 * hkg::orth_norm_parts());
+    return l;
+}
+
+// A 256-row panel is read through a 32-bit buffer range.
+bool sizes_fit(int64_t rows, int64_t cols)
+{
+    constexpr int64_t kMax = (int64_t(1) << 31) / (256 * 2) - 64;
+    return rows <= kMax && cols <= kMax;
+}
+
+// The tile of a product (M x N, or the triangle of an M x M): the one whose rounds
+// of the 256 compute units take least, a unit's time for a tile growing with its
+// area and, for smaller tiles, with the LDS bytes per matrix instruction (two
+// 128-tiles share a compute unit).
+int pick_tile(int64_t M, int64_t N, bool triangle)
+{
+    int best = 256;
+    double least = 0.0;
+    for (const int t : {256, 192, 128}) {
+        const int64_t gm = ceil_div(M, t), gn = ceil_div(N, t), tiles = triangle ? gm * (gm + 1) / 2 : gm * gn;
+        const double cost = (double)ceil_div(tiles, 256) * t * t * (t == 256 ? 1.0 : t == 192 ? 1.05 : 1.2);
+        if (least == 0.0 || cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+}  // namespace hkg::api
+
+using namespace hkg::api;
+
+extern "C" {
+
+int64_t hkg_orthogonalize_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows < 0 || cols < 0)
+        return HKG_ERR_SHAPE;
+    if (!sizes_fit(rows, cols))
+        return HKG_ERR_SIZE;
+    return rows == 0 || cols == 0 ? 0 : layout(rows, cols).bytes;
+}
+
+int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type, int64_t ldg,
+                      int32_t steps, float a, float b, float c, float eps, void *out, int64_t ldo,
+                      void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int64_t e = elem_size(g_type);
+    if (!e || steps < 0 || steps > 64 || !(eps >= 0.0f))
+        return HKG_ERR_OPTS;
+    if (rows < 0 || cols < 0)
+        return HKG_ERR_SHAPE;
+    if (rows == 0 || cols == 0)
+        return HKG_OK;
+    if (!G || !out || !workspace)
+        return HKG_ERR_NULL;
+    int rc = check_matrix(G, rows, cols, e, &ldg);
+    if (rc == HKG_OK)
+        rc = check_matrix(out, rows, cols, 2, &ldo);
+    if (rc != HKG_OK)
+        return rc;
+    if (!aligned16(workspace))
+        return HKG_ERR_ALIGN;
+    if (!sizes_fit(rows, cols))
+        return HKG_ERR_SIZE;
+    const OrthLayout l = layout(rows, cols);
+    if (workspace_bytes < l.bytes)
+        return HKG_ERR_WORKSPACE;
+    // G is read to the end before out is written, except with no steps at all,
+    // where each element is read and written by one lane: G itself is a valid out
+    const bool same = out == G && g_type == HKG_T_BF16 && ldo == ldg;
+    const int64_t ob = extent(rows, cols, ldo, 2), gb = extent(rows, cols, ldg, e);
+    if ((!same && overlaps(out, ob, G, gb)) || overlaps(workspace, l.bytes, G, gb) ||
+        overlaps(workspace, l.bytes, out, ob))
+        return HKG_ERR_OVERLAP;
+    rc = prepare_launch(stream);
+    if (rc != HKG_OK)
+        return rc;
+
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    uint16_t *x = reinterpret_cast<uint16_t *>(ws + l.x), *am = reinterpret_cast<uint16_t *>(ws + l.a),
+             *pm = reinterpret_cast<uint16_t *>(ws + l.p);
+    uint16_t *xt[2] = {reinterpret_cast<uint16_t *>(ws + l.xt[0]), reinterpret_cast<uint16_t *>(ws + l.xt[1])};
+    double *sums = reinterpret_cast<double *>(ws + l.sums);
+    const hkg::ElemType t = g_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16;
+    const hkg::OrthInput in = {G, ldg, static_cast<int>(rows), static_cast<int>(cols)};
+    const bool tall = rows > cols;
+    const int m = static_cast<int>(l.m), n = static_cast<int>(l.n), mp = static_cast<int>(l.mp),
+              np = static_cast<int>(l.np);
+
+    rc = launched(hkg::launch_orth_norm(t, in, sums, st));
+    if (rc != HKG_OK)
+        return rc;
+    if (steps == 0)
+        return launched(hkg::launch_orth_convert(t, in, sums, eps, nullptr, 0, nullptr, 0,
+                                                 static_cast<uint16_t *>(out), ldo, st));
+    rc = launched(tall ? hkg::launch_orth_convert(t, in, sums, eps, xt[0], mp, x, np, nullptr, 0, st)
+                       : hkg::launch_orth_convert(t, in, sums, eps, x, np, xt[0], mp, nullptr, 0, st));
+
+    const float s = 1.0f / hkg::kOrthScale;   // a product of two scaled operands carries it twice
+    const int sym = pick_tile(m, m, true), upd = pick_tile(m, n, false);
+    for (int i = 0; i < steps && rc == HKG_OK; ++i) {
+        const bool last = i + 1 == steps;
+        const _Float16 *x16 = reinterpret_cast<const _Float16 *>(x);
+        // A = X X^T
+        rc = launched(hkg::launch_orth_product(sym, order_of(m, m, 2 * np, sym), true, {x, x, m, m, np},
+                                               {s, 0.0f, nullptr, 0, am, mp, mp, am, mp, mp, 0}, st));
+        // P = b A + c A A
+        if (rc == HKG_OK)
+            rc = launched(hkg::launch_orth_product(
+                sym, order_of(m, m, 2 * mp, sym), true, {am, am, m, m, mp},
+                {c * s, b, reinterpret_cast<const _Float16 *>(am), mp, pm, mp, mp, pm, mp, mp, 0}, st));
+        // X <- a X + P X, as X and X^T, or the result in its own orientation
+        hkg::OrthEpilogue ep = {s, a, x16, np, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
+        if (last) {
+            ep = {s * s, a * s, x16, np, nullptr, 0, 0, nullptr, 0, 0, 1};
+            if (tall) {
+                ep.transposed = static_cast<uint16_t *>(out);
+                ep.ldt = ldo;
+                ep.cols_t = m;
+            } else {
+                ep.straight = static_cast<uint16_t *>(out);
+                ep.lds = ldo;
+                ep.cols_s = n;
+            }
+        }
+        if (rc == HKG_OK)
+            rc = launched(hkg::launch_orth_product(upd, order_of(m, n, 2 * mp, upd), false,
+                                                   {pm, xt[i & 1], m, n, mp}, ep, st));
+    }
+    return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,300 @@
+// orth_kernels.hip -- gfx950 kernels of the orthogonalised update: the norm, the
+// conversion to scaled fp16 (with the transpose), and the three products of a
+// step on tile16.h's loop.
+//
+// With m <= n the smaller and larger side, one step is
+//   A = X X^T           m x m, symmetric: only tiles on and above the diagonal
+//   P = b A + c A A     m x m, symmetric
+//   X <- a X + P X      m x n
+// The loop wants both operands with K contiguous: X [m][n] for the first, A for
+// the second, P (symmetric) and X^T [n][m] for the third, so the third product's
+// epilogue writes X and X^T, and the first two write each off-diagonal tile twice.
+// X, A and P are fp16, each times 2^12: their largest entries stay below 2^16
+// while singular values stay below 2, and entries of X near 1 / sqrt(m n) or of A
+// near 1 / (m sqrt n) stay clear of fp16's subnormals.  fp16 instead of bf16
+// because all three are bounded: 11 significand bits at the same rate.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "orth_kernels.h"
+#include "tile16.h"
+
+namespace hkg {
+namespace {
+
+// ---- |G|^2: partial sums in 64 bits, joined in a fixed order -----------------
+template <int kElem>
+__global__ __launch_bounds__(256) void orth_norm_kernel(const OrthInput p, double *partial)
+{
+    double s = 0.0;
+    const int64_t vecs = (p.cols + 7) / 8, total = vecs * p.rows;
+    const bool vec = (((reinterpret_cast<uintptr_t>(p.G)) | (uintptr_t)(p.ldg * (kElem == 0 ? 2 : 4))) & 15) == 0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int row = (int)(i / vecs), col = 8 * (int)(i % vecs);
+        const Vec8<kElem> v = load8<kElem>(p.G, p.ldg, row, p.rows, col, p.cols, vec);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t b;
+            if constexpr (kElem == 0)
+                b = e & 1 ? v.w[e >> 1] & 0xffff0000u : v.w[e >> 1] << 16;
+            else
+                b = v.w[e];
+            const double f = (double)__builtin_bit_cast(float, b);
+            s += f * f;
+        }
+    }
+    __shared__ double sums[256];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if (threadIdx.x < d)
+            sums[threadIdx.x] += sums[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        partial[blockIdx.x] = sums[0];
+}
+
+// ---- X = G / (|G| + eps) in scaled fp16, and its transpose -------------------
+// A 64 x 64 tile a workgroup: rows x ps (straight) and cols x pt (transposed),
+// zeros past the matrix.  out: with no steps at all, the bf16 result itself.
+template <int kElem>
+__global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, const double *partial, int parts,
+                                                           float eps, _Float16 *straight, int ps, _Float16 *transposed,
+                                                           int pt, uint16_t *out, int64_t ldo)
+{
+    __shared__ double sums[256];
+    __shared__ float tile[64][65];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 256)
+        s += partial[i];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if (threadIdx.x < d)
+            sums[threadIdx.x] += sums[threadIdx.x + d];
+        __syncthreads();
+    }
+    // a norm that is no number makes every element NaN; a zero matrix stays zero
+    const double norm = sqrt(sums[0]);
+    const double inv = norm > 0.0 ? 1.0 / (norm + (double)eps) : 0.0;
+    const double mul = norm == 0.0 ? 0.0 : isfinite(norm) ? inv : (double)NAN;
+    const double scaled = mul * kOrthScale;
+    const int tc = (p.cols + 63) / 64, r0 = blockIdx.x / tc * 64, c0 = blockIdx.x % tc * 64;
+    const bool vec = (((reinterpret_cast<uintptr_t>(p.G)) | (uintptr_t)(p.ldg * (kElem == 0 ? 2 : 4))) & 15) == 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int rl = (threadIdx.x >> 3) + 32 * h, cl = 8 * (threadIdx.x & 7);
+        const int row = r0 + rl, col = c0 + cl;
+        const Vec8<kElem> v = load8<kElem>(p.G, p.ldg, row, p.rows, col, p.cols, vec);
+        f16x8_t x;
+        uint16_t y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t b;
+            if constexpr (kElem == 0)
+                b = e & 1 ? v.w[e >> 1] & 0xffff0000u : v.w[e >> 1] << 16;
+            else
+                b = v.w[e];
+            const double f = (double)__builtin_bit_cast(float, b);
+            x[e] = (_Float16)(float)(f * scaled);
+            tile[rl][cl + e] = (float)x[e];
+            y[e] = (uint16_t)pack2_bf16((float)(f * mul), 0.f);
+        }
+        if (row < p.rows) {
+            if (straight)
+                *reinterpret_cast<f16x8_t *>(straight + (int64_t)row * ps + col) = x;
+            if (out)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < p.cols)
+                        out[row * ldo + col + e] = y[e];
+        }
+    }
+    if (!transposed)
+        return;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int cl = (threadIdx.x >> 3) + 32 * h, rl = 8 * (threadIdx.x & 7);
+        if (c0 + cl >= p.cols)
+            continue;
+        f16x8_t x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = (_Float16)tile[rl + e][cl];
+        *reinterpret_cast<f16x8_t *>(transposed + (int64_t)(c0 + cl) * pt + r0 + rl) = x;
+    }
+}
+
+// ---- a product of a step -----------------------------------------------------
+// v = alpha acc + beta D, stored as rows (straight) and/or as columns (transposed).
+// Columns are stored through LDS: a wave writes its rows there as 16-byte units,
+// unit u of row r in place u ^ r ^ (r >> 3) (so that neither the row writes nor the
+// column reads below share a bank), and reads 8 rows of a column back for each
+// 16-byte store of 8 consecutive elements.
+template <int kB, bool kBf16>
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
+{
+    u32x4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kBf16) {
+            w[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+        } else {
+            const f16x2_t h = {(_Float16)v[2 * i], (_Float16)v[2 * i + 1]};
+            w[i] = __builtin_bit_cast(uint32_t, h);
+        }
+    }
+    return w;
+}
+
+__device__ __forceinline__ void store8(uint16_t *p, const u32x4_t &v, int n, bool vec)
+{
+    if (vec && n >= 8) {
+        *reinterpret_cast<u32x4_t *>(p) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+template <int kT, bool kBf16>
+__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(const TileOperands o, const OrthEpilogue p)
+{
+    using Loop = TileLoop<F16, kT>;
+    constexpr int kB = Loop::kB, kSide = 16 * kB;   // a wave's quarter: kSide x kSide
+    constexpr int kPitch = kB == 4 ? 64 : 128;      // its rows in LDS: a power of two of units
+    static_assert(4 * kSide * kPitch * 2 <= Loop::kLds, "the four quarters fit the ring");
+    __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
+    int tm, tn;
+    if (o.triangle)
+        triangle_tile(blockIdx.x, o.Gm, tm, tn);
+    else
+        remap_tile(blockIdx.x, o.Gm, o.Gn, o.W, o.C, tm, tn);
+    f32x4_t acc[kB][kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    Loop loop;
+    loop.init(o, smem, tm, tn);
+    loop.run(acc, o.nk);
+    settle(acc);
+    const int x = loop.lane & 15, q = loop.lane >> 4;
+    const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
+    const bool columns = p.transposed && !(o.triangle && tm == tn && p.straight);
+    if (columns)
+        barrier();   // every wave has read its last fragments
+    uint16_t *lds = reinterpret_cast<uint16_t *>(smem) + loop.wave * kSide * kPitch;
+    const bool vec_s = ((reinterpret_cast<uintptr_t>(p.straight) | (uintptr_t)(2 * p.lds)) & 15) == 0;
+    const bool vec_t = ((reinterpret_cast<uintptr_t>(p.transposed) | (uintptr_t)(2 * p.ldt)) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+        const int rl = 16 * i + x, row = row0 + rl;
+        settle_row(acc, i);
+#pragma unroll
+        for (int h = 0; h < kB / 2; ++h) {
+            const int cl = 32 * h + 8 * q, col = col0 + cl;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = p.alpha * acc[i][2 * h][e];
+                v[4 + e] = p.alpha * acc[i][2 * h + 1][e];
+            }
+            if (p.D && row < o.rows_a && col < p.ldd) {
+                const f16x8_t d = *reinterpret_cast<const f16x8_t *>(p.D + (int64_t)row * p.ldd + col);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += p.beta * (float)d[e];
+            }
+            const u32x4_t w = pack8<kB, kBf16>(v);
+            if (p.straight && row < o.rows_a)
+                store8(p.straight + row * p.lds + col, w, p.cols_s - col, vec_s);
+            if (columns)
+                *reinterpret_cast<u32x4_t *>(lds + rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1))) = w;
+        }
+    }
+    if (!columns)
+        return;
+    wait_lds();   // the region is this wave's own
+    constexpr int kUnits = kSide / 8;   // 8-row units of a column
+#pragma unroll 4
+    for (int k = loop.lane; k < kSide * kUnits; k += 64) {
+        const int u = k % kUnits, cl = k / kUnits;
+        u32x4_t w = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int rl = 8 * u + e;
+            const uint32_t t = lds[rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1)) + (cl & 7)];
+            w[e >> 1] |= t << (16 * (e & 1));
+        }
+        const int col = col0 + cl, row = row0 + 8 * u;
+        if (col < o.rows_b)
+            store8(p.transposed + col * p.ldt + row, w, p.cols_t - row, vec_t);
+    }
+}
+
+}  // namespace
+
+constexpr int kNormParts = 512;
+int orth_norm_parts() { return kNormParts; }
+
+hipError_t launch_orth_norm(ElemType t, const OrthInput &p, double *partial, hipStream_t stream)
+{
+    if (t == kElemBf16)
+        hipLaunchKernelGGL(orth_norm_kernel<0>, dim3(kNormParts), dim3(256), 0, stream, p, partial);
+    else
+        hipLaunchKernelGGL(orth_norm_kernel<1>, dim3(kNormParts), dim3(256), 0, stream, p, partial);
+    return hipGetLastError();
+}
+
+hipError_t launch_orth_convert(ElemType t, const OrthInput &p, const double *partial, float eps, void *straight, int ps,
+                               void *transposed, int pt, uint16_t *out, int64_t ldo, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((p.rows + 63) / 64) * (unsigned)((p.cols + 63) / 64)), block(256);
+    auto s = static_cast<_Float16 *>(straight), tr = static_cast<_Float16 *>(transposed);
+    if (t == kElemBf16)
+        hipLaunchKernelGGL(orth_convert_kernel<0>, grid, block, 0, stream, p, partial, kNormParts, eps, s, ps, tr, pt,
+                           out, ldo);
+    else
+        hipLaunchKernelGGL(orth_convert_kernel<1>, grid, block, 0, stream, p, partial, kNormParts, eps, s, ps, tr, pt,
+                           out, ldo);
+    return hipGetLastError();
+}
+
+template <bool kBf16>
+static hipError_t launch_product(int tile, const TileOperands &o, const OrthEpilogue &e, hipStream_t stream)
+{
+    const dim3 grid(o.triangle ? (unsigned)o.Gm * (unsigned)(o.Gm + 1) / 2 : (unsigned)o.Gm * (unsigned)o.Gn), block(256);
+    if (tile == 256)
+        hipLaunchKernelGGL((orth_product_kernel<256, kBf16>), grid, block, 0, stream, o, e);
+    else if (tile == 192)
+        hipLaunchKernelGGL((orth_product_kernel<192, kBf16>), grid, block, 0, stream, o, e);
+    else
+        hipLaunchKernelGGL((orth_product_kernel<128, kBf16>), grid, block, 0, stream, o, e);
+    return hipGetLastError();
+}
+
+hipError_t launch_orth_product(int tile, const TileOrder &order, bool triangle, const OrthProduct &p,
+                               const OrthEpilogue &e, hipStream_t stream)
+{
+    TileOperands o = {};
+    o.A = p.A;
+    o.B = p.B;
+    o.pitch_a = o.pitch_b = o.kb = 2 * p.K;
+    o.rows_a = p.M;
+    o.rows_b = p.N;
+    o.Gm = order.Gm;
+    o.Gn = order.Gn;
+    o.W = order.W;
+    o.C = order.C;
+    o.nk = p.K / 64;
+    o.triangle = triangle;
+    return e.bf16 ? launch_product<true>(tile, o, e, stream) : launch_product<false>(tile, o, e, stream);
+}
+
+}  // namespace hkg

@@ -1,5 +1,5 @@
-"""Python binding of include/hkg_ops.h: the MXFP4 linear layer on GPU
-tensors.
+"""Python binding of include/hkg_ops.h: the MXFP4 linear layer and the
+orthogonalised weight update, on GPU tensors.
 
 An MXFP4 matrix is a pair (codes, packed): uint8 [rows, Kp / 2] with two e2m1
 codes a byte (Kp = K rounded up to 32) and its E8M0 scales in packed order.
@@ -8,6 +8,7 @@ codes a byte (Kp = K rounded up to 32) and its E8M0 scales in packed order.
     x, sx, xt, sxt = mxfp4_quantize_both(X, A, B)        # a training step's input
     y = gemm_mxfp4(x, w, sx, sw)                         # its forward product
     dx, dw = linear_mxfp4_backward(dy, wt, swt, xt, sxt)
+    W -= lr * orthogonalize(momentum)
     y = linear_mxfp4(X, w, sw)                           # serving, from one row up
 
 with A, B = HKG_MX_OPERAND_A, HKG_MX_OPERAND_B.  Every function takes `stream`
@@ -37,6 +38,8 @@ OPS_EXPORTS = (
     "hkg_linear_mxfp4",
     "hkg_linear_mxfp4_backward_workspace_bytes",
     "hkg_linear_mxfp4_backward",
+    "hkg_orthogonalize_workspace_bytes",
+    "hkg_orthogonalize",
 )
 
 _ready = None
@@ -59,6 +62,8 @@ def _lib() -> ctypes.CDLL:
             "hkg_linear_mxfp4_backward_workspace_bytes": [i64, i64, i64],
             "hkg_linear_mxfp4_backward": [i64, i64, i64, p, i32, i64, p, p, p, p, p, i64, p, i64, p,
                                           i64, p],
+            "hkg_orthogonalize_workspace_bytes": [i64, i64],
+            "hkg_orthogonalize": [i64, i64, p, i32, i64, i32, f32, f32, f32, f32, p, i64, p, i64, p],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -257,3 +262,26 @@ def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, 
     _check(_lib().hkg_linear_mxfp4_backward(M, N, K, pdy, t, lddy, pw, psw, px, psx, pdx, lddx, pdw,
                                             lddw, pws, nws, on.handle), "hkg_linear_mxfp4_backward")
     return dx, dw
+
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None, workspace=None,
+                  stream=None):
+    """The orthogonalised direction of an update G [rows, cols] (bf16 or fp32): X =
+    G / (|G| + eps), then `steps` times X <- a X + (b A + c A A) X with A = X Xᵀ
+    (on Gᵀ where G is tall); bf16, in `out` (which may be G).  workspace: a uint8
+    tensor of hkg_orthogonalize_workspace_bytes(rows, cols)."""
+    import torch
+    t = _elem_type(G, "G")
+    pg, ldg = _hkg._matrix(G, "G")
+    rows, cols = G.shape
+    a, b, c = coefficients
+    on = _On(stream, G.device)
+    out, po, ldo = _output(on, out, (rows, cols), torch.bfloat16, "out")
+    need = _check(_lib().hkg_orthogonalize_workspace_bytes(rows, cols), "hkg_orthogonalize_workspace_bytes")
+    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
+    _check(_lib().hkg_orthogonalize(rows, cols, pg, t, ldg, steps, a, b, c, eps, po, ldo, pws, nws, on.handle),
+           "hkg_orthogonalize")
+    return out

@@ -1,8 +1,9 @@
 /*
  * hkg_ops.h -- C ABI of the operators around the GEMM of hkg.h: the MXFP4
- * linear layer (quantisation, product, few-token form, gradients).  Same
- * library, same conventions: device pointers owned by the caller, every
- * argument checked before the first HIP call, work enqueued on `stream` and never waited for, HKG_OK or a negative
+ * linear layer (quantisation, product, few-token form, gradients) and the
+ * orthogonalised weight update.  Same library, same conventions: device
+ * pointers owned by the caller, every argument checked before the first HIP
+ * call, work enqueued on `stream` and never waited for, HKG_OK or a negative
  * hkg_status returned.  Intermediate results live in a workspace that the
  * caller passes (16-byte aligned, at least the bytes the matching
  * *_workspace_bytes function returns, used until the stream has passed the
@@ -113,6 +114,28 @@ int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, i
                               int64_t lddy, const void *Wt, const void *SWt, const void *Xt,
                               const void *SXt, void *dx, int64_t lddx, void *dw, int64_t lddw,
                               void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * The orthogonalised direction of an update (the Muon optimiser's step):
+ * X = G / (|G|_F + eps), then `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X
+ * on G, or on G^T where G has more rows than columns, and out = X (bf16).  The
+ * odd polynomial drives every singular value of X towards 1 while its singular
+ * vectors stay.
+ *   G    [rows][cols] bf16 or fp32 (g_type), rows ldg elements apart (0 = cols)
+ *   out  [rows][cols] bf16, rows ldo elements apart (0 = cols); may be G itself
+ *        when both are bf16 with one pitch, else must not overlap it
+ *   steps 0 .. 64; eps >= 0 (a zero matrix stays zero)
+ * X, A and b A + c A A are kept in fp16 between products (11-bit significands,
+ * scaled by a power of two), sums are fp32; the polynomial must keep the
+ * singular values of X below 2 and those of b A + c A A below 16 (beyond that
+ * fp16 overflows to infinity), as the usual coefficients (3.4445, -4.7750,
+ * 2.0315) do.  A NaN or an infinity in G makes every element of out NaN.
+ */
+int64_t hkg_orthogonalize_workspace_bytes(int64_t rows, int64_t cols);
+int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type, int64_t ldg,
+                      int32_t steps, float a, float b, float c, float eps, void *out, int64_t ldo,
+                      void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -131,3 +131,28 @@ def backward(M=64, N=64, K=64, dy=P[0], t=0, lddy=0, Wt=P[1], SWt=P[2], Xt=P[3],
 ])
 def test_backward_refusals(kw, status):
     assert backward(**kw) == status
+
+
+def orth(rows=64, cols=96, G=P[0], t=0, ldg=0, steps=5, eps=1e-7, out=P[1], ldo=0, ws=P[2], n=BIG):
+    return lib().hkg_orthogonalize(rows, cols, G, t, ldg, steps, 3.4445, -4.775, 2.0315, eps, out, ldo, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(t=2), hkg.HKG_ERR_OPTS), (dict(steps=-1), hkg.HKG_ERR_OPTS), (dict(steps=65), hkg.HKG_ERR_OPTS),
+    (dict(eps=-1.0), hkg.HKG_ERR_OPTS), (dict(eps=float("nan")), hkg.HKG_ERR_OPTS),
+    (dict(rows=-1), hkg.HKG_ERR_SHAPE), (dict(G=None), hkg.HKG_ERR_NULL), (dict(out=None), hkg.HKG_ERR_NULL),
+    (dict(ws=None), hkg.HKG_ERR_NULL), (dict(n=1 << 10), hkg.HKG_ERR_WORKSPACE), (dict(ws=P[2] + 8), hkg.HKG_ERR_ALIGN),
+    (dict(G=P[0] + 1), hkg.HKG_ERR_ALIGN), (dict(ldg=95), hkg.HKG_ERR_OPTS), (dict(ldo=95), hkg.HKG_ERR_OPTS),
+    (dict(rows=1 << 23), hkg.HKG_ERR_SIZE), (dict(cols=(1 << 63) - 1), hkg.HKG_ERR_SIZE),
+    (dict(out=P[0] + 2), hkg.HKG_ERR_OVERLAP), (dict(out=P[0], t=1), hkg.HKG_ERR_OVERLAP),
+    (dict(out=P[0], ldo=100), hkg.HKG_ERR_OVERLAP), (dict(ws=P[0]), hkg.HKG_ERR_OVERLAP), (dict(ws=P[1]), hkg.HKG_ERR_OVERLAP),
+    (dict(rows=0, G=None, ws=None), hkg.HKG_OK),
+])
+def test_orthogonalize_refusals(kw, status):
+    assert orth(**kw) == status
+
+
+def test_orthogonalize_workspace_size():
+    f = lib().hkg_orthogonalize_workspace_bytes
+    assert f(64, 64) >= 5 * 64 * 64 * 2 and f(100, 30) == f(30, 100) and f(0, 5) == 0
+    assert f(-1, 5) == hkg.HKG_ERR_SHAPE and f(1 << 23, 5) == hkg.HKG_ERR_SIZE
