@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
 // unit u of row r in place u ^ r ^ (r >> 3) (so that neither the row writes nor the
 // column reads below share a bank), and reads 8 rows of a column back for each
 // 16-byte store of 8 consecutive elements.
-template <int kB, bool kBf16>
+template <bool kBf16>
 __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
 {
     u32x4_t w;
@@ -149,16 +149,13 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
     return w;
 }
 
-__device__ __forceinline__ void store8(uint16_t *p, const u32x4_t &v, int n, bool vec)
+// The first n of 8 elements, one by one (a result whose rows are not whole units).
+__device__ __forceinline__ void store_part(uint16_t *p, const u32x4_t &v, int n)
 {
-    if (vec && n >= 8) {
-        *reinterpret_cast<u32x4_t *>(p) = v;
-    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n)
-                p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
 }
 
 template <int kT, bool kBf16>
@@ -187,33 +184,52 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
     const int x = loop.lane & 15, q = loop.lane >> 4;
     const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
     const bool columns = p.transposed && !(o.triangle && tm == tn && p.straight);
+    // Buffers over the wave's rows of D and of the straight result: rows past the
+    // matrix read zeros and drop stores, as do column units past it (lane offset
+    // kPastEnd), so nothing below branches.
+    const int rows = o.rows_a - row0;
+    auto over = [&](const void *base, int64_t ld) {
+        return buffer_of(static_cast<const uint16_t *>(base) + row0 * ld + col0,
+                         base && rows > 0 ? (uint32_t)min(rows, kSide) * (uint32_t)(2 * ld) : 0u);
+    };
+    auto lane_off = [&](int h, int64_t ld, int cols) {
+        return col0 + 32 * h + 8 * q < cols ? (int)(2 * (x * ld + 32 * h + 8 * q)) : kPastEnd;
+    };
+    auto row_off = [&](int i, int64_t ld) { return __builtin_amdgcn_readfirstlane((int)(32 * i * ld)); };
+    // D's part of the tile, all of it at once: the fragments' registers are free
+    u32x4_t d[kB][kB / 2];
+    const __amdgpu_buffer_rsrc_t rd = over(p.D, p.ldd);
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int h = 0; h < kB / 2; ++h)
+            d[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rd, lane_off(h, p.ldd, (int)p.ldd), row_off(i, p.ldd), 0);
     if (columns)
         barrier();   // every wave has read its last fragments
     uint16_t *lds = reinterpret_cast<uint16_t *>(smem) + loop.wave * kSide * kPitch;
-    const bool vec_s = ((reinterpret_cast<uintptr_t>(p.straight) | (uintptr_t)(2 * p.lds)) & 15) == 0;
-    const bool vec_t = ((reinterpret_cast<uintptr_t>(p.transposed) | (uintptr_t)(2 * p.ldt)) & 15) == 0;
+    // whole 16-byte units in 16-byte aligned rows (always so in the workspace)
+    const bool units_s = ((reinterpret_cast<uintptr_t>(p.straight) | (uintptr_t)(2 * p.lds) | (uintptr_t)(2 * p.cols_s)) & 15) == 0 &&
+                         p.lds < (1 << 22);
+    const bool units_t = ((reinterpret_cast<uintptr_t>(p.transposed) | (uintptr_t)(2 * p.ldt) | (uintptr_t)(2 * p.cols_t)) & 15) == 0 &&
+                         p.ldt < (1 << 22);
+    const __amdgpu_buffer_rsrc_t rs = over(units_s ? p.straight : nullptr, p.lds);
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
-        const int rl = 16 * i + x, row = row0 + rl;
+        const int rl = 16 * i + x;
         settle_row(acc, i);
 #pragma unroll
         for (int h = 0; h < kB / 2; ++h) {
-            const int cl = 32 * h + 8 * q, col = col0 + cl;
+            const int cl = 32 * h + 8 * q;
+            const f16x8_t dv = __builtin_bit_cast(f16x8_t, d[i][h]);
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] = p.alpha * acc[i][2 * h][e];
-                v[4 + e] = p.alpha * acc[i][2 * h + 1][e];
-            }
-            if (p.D && row < o.rows_a && col < p.ldd) {
-                const f16x8_t d = *reinterpret_cast<const f16x8_t *>(p.D + (int64_t)row * p.ldd + col);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] += p.beta * (float)d[e];
-            }
-            const u32x4_t w = pack8<kB, kBf16>(v);
-            if (p.straight && row < o.rows_a)
-                store8(p.straight + row * p.lds + col, w, p.cols_s - col, vec_s);
+            for (int e = 0; e < 8; ++e)
+                v[e] = p.alpha * acc[i][2 * h + (e >> 2)][e & 3] + p.beta * (float)dv[e];
+            const u32x4_t w = pack8<kBf16>(v);
+            if (units_s)
+                __builtin_amdgcn_raw_buffer_store_b128(w, rs, lane_off(h, p.lds, p.cols_s), row_off(i, p.lds), 0);
+            else if (p.straight && rl < rows)
+                store_part(p.straight + (row0 + rl) * p.lds + col0 + cl, w, p.cols_s - col0 - cl);
             if (columns)
                 *reinterpret_cast<u32x4_t *>(lds + rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1))) = w;
         }
@@ -222,6 +238,10 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
         return;
     wait_lds();   // the region is this wave's own
     constexpr int kUnits = kSide / 8;   // 8-row units of a column
+    const int tcols = o.rows_b - col0;  // columns of the tile that exist: rows of the transposed result
+    const __amdgpu_buffer_rsrc_t rt =
+        buffer_of(p.transposed + col0 * p.ldt + row0,
+                  units_t && tcols > 0 ? (uint32_t)min(tcols, kSide) * (uint32_t)(2 * p.ldt) : 0u);
 #pragma unroll 4
     for (int k = loop.lane; k < kSide * kUnits; k += 64) {
         const int u = k % kUnits, cl = k / kUnits;
@@ -232,9 +252,11 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
             const uint32_t t = lds[rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1)) + (cl & 7)];
             w[e >> 1] |= t << (16 * (e & 1));
         }
-        const int col = col0 + cl, row = row0 + 8 * u;
-        if (col < o.rows_b)
-            store8(p.transposed + col * p.ldt + row, w, p.cols_t - row, vec_t);
+        if (units_t)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                w, rt, row0 + 8 * u < p.cols_t ? (int)(2 * (cl * p.ldt + 8 * u)) : kPastEnd, 0, 0);
+        else if (cl < tcols)
+            store_part(p.transposed + (int64_t)(col0 + cl) * p.ldt + row0 + 8 * u, w, p.cols_t - row0 - 8 * u);
     }
 }
 

@@ -19,7 +19,6 @@ wrong kind); nothing has run then.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import dense_gemm_fp8_amd as _hkg
@@ -43,11 +42,12 @@ OPS_EXPORTS = (
 )
 
 _ready = None
+_raw_stream = None       # device index -> handle of torch's current stream there
 
 
 def _lib() -> ctypes.CDLL:
     """libhkg with the argument types of hkg_ops.h set."""
-    global _ready
+    global _ready, _raw_stream
     if _ready is None:
         lib = _hkg.load()
         i64, i32, p, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
@@ -69,6 +69,11 @@ def _lib() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = i64 if name.endswith("_bytes") else ctypes.c_int
+        import torch
+        # the handle alone costs a tenth of a torch Stream object, which is a good
+        # part of a small call's time on the host
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         _ready = lib
     return _ready
 
@@ -80,72 +85,81 @@ def _check(rc, name):
 
 
 def _pad32(k: int) -> int:
-    return -(-k // 32) * 32
+    return (k + 31) & ~31
+
+
+def _scale_bytes(rows: int, kp: int) -> int:
+    """hkg_mx_packed_scale_bytes for sizes the call itself will check."""
+    return ((rows + 127) >> 7) * ((kp + 127) >> 7) * 512
 
 
 def _elem_type(t, name) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return HKG_T_BF16
-    if t.dtype == torch.float32:
+    if dt is torch.float32:
         return HKG_T_F32
     raise TypeError("%s must be bfloat16 or float32" % name)
 
 
 def _codes(t, rows, K, name):
-    """Pointer of the codes of a [rows, K] MXFP4 matrix (K None: any)."""
+    """Pointer of the codes of a [rows, K] MXFP4 matrix."""
     import torch
-    if t.dtype != torch.uint8 or t.dim() != 2:
+    if t.dtype is not torch.uint8 or t.dim() != 2:
         raise TypeError("%s must be a 2-D uint8 tensor of e2m1 codes" % name)
-    if t.shape[0] != rows or t.shape[1] != _pad32(K) // 2:
-        raise ValueError("%s must be [%d, %d]" % (name, rows, _pad32(K) // 2))
+    if tuple(t.shape) != (rows, _pad32(K) >> 1):
+        raise ValueError("%s must be [%d, %d]" % (name, rows, _pad32(K) >> 1))
     return _hkg._dev_ptr(t, name)
 
 
 def _packed(t, rows, K, name):
     import torch
-    need = _hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K))
-    if t.dtype != torch.uint8 or (need >= 0 and t.numel() < need):
+    need = _scale_bytes(rows, _pad32(K))
+    if t.dtype is not torch.uint8 or t.numel() < need:
         raise ValueError("%s must be a uint8 tensor of at least %d bytes" % (name, need))
     return _hkg._dev_ptr(t, name)
 
 
-class _On:
-    """The stream a call runs on: its handle, and allocations that belong to it
-    (a block freed while the stream still uses it is then reused in its order)."""
-
-    def __init__(self, stream, device):
-        import torch
-        self._torch, self._device = torch, device
-        self._stream = stream
-        self.handle = _hkg._stream_handle(stream)
-
-    def empty(self, shape, dtype):
-        ctx = self._torch.cuda.stream(self._stream) if self._stream is not None else contextlib.nullcontext()
-        with ctx:
-            return self._torch.empty(shape, dtype=dtype, device=self._device)
-
-    def bytes(self, n):
-        return self.empty((max(int(n), 16),), self._torch.uint8)
+def _handle(stream, t) -> int:
+    """Handle of the stream a call runs on: `stream`, or torch's current one on t's device."""
+    _lib()
+    return int(stream.cuda_stream) if stream is not None else _raw_stream(t.get_device())
 
 
-def _output(on, t, shape, dtype, name):
+def _empty(shape, dtype, like, stream):
+    """A new tensor on like's device that belongs to the stream the call runs on (a
+    block freed while that stream still uses it is then reused in its order)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _bytes(n, like, stream):
+    import torch
+    return _empty((max(int(n), 16),), torch.uint8, like, stream)
+
+
+def _output(t, shape, dtype, name, like, stream):
     """t, or a new tensor; -> (tensor, pointer, row pitch)."""
     if t is None:
-        t = on.empty(shape, dtype)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError("%s must be a %s tensor of shape %s" % (name, dtype, tuple(shape)))
+        t = _empty(shape, dtype, like, stream)
+        return t, t.data_ptr(), shape[1]
+    if tuple(t.shape) != shape or t.dtype is not dtype:
+        raise ValueError("%s must be a %s tensor of shape %s" % (name, dtype, shape))
     ptr, ld = _hkg._matrix(t, name)
     return t, ptr, ld
 
 
-def _workspace(on, t, need, name):
-    """Pointer and size of the caller's workspace, or of a new one."""
+def _workspace(t, need, like, stream):
+    """(tensor, pointer, size) of the caller's workspace, or of a new one."""
     if need <= 0:
         return None, None, 0
     if t is None:
-        t = on.bytes(need)
-    return t, _hkg._dev_ptr(t, name), t.numel() * t.element_size()
+        t = _bytes(need, like, stream)
+    return t, _hkg._dev_ptr(t, "workspace"), t.numel() * t.element_size()
 
 
 def mxfp4_quantize(x, operand, stream=None):
@@ -155,12 +169,11 @@ def mxfp4_quantize(x, operand, stream=None):
     xt = _elem_type(x, "x")
     px, ld = _hkg._matrix(x, "x")
     rows, K = x.shape
-    on = _On(stream, x.device)
-    _check(_lib().hkg_mxfp4_code_bytes(rows, K), "hkg_mxfp4_code_bytes")
-    codes = on.empty((rows, _pad32(K) // 2), torch.uint8)
-    packed = on.bytes(_hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K)))
+    st = _handle(stream, x)
+    codes = _empty((rows, _pad32(K) >> 1), torch.uint8, x, stream)
+    packed = _bytes(_scale_bytes(rows, K), x, stream)
     _check(_lib().hkg_mxfp4_quantize(operand, rows, K, px, xt, ld, codes.data_ptr(), packed.data_ptr(),
-                                     on.handle), "hkg_mxfp4_quantize")
+                                     st), "hkg_mxfp4_quantize")
     return codes, packed
 
 
@@ -171,16 +184,14 @@ def mxfp4_quantize_both(x, operand, operand_t, stream=None):
     xt = _elem_type(x, "x")
     px, ld = _hkg._matrix(x, "x")
     rows, K = x.shape
-    on = _On(stream, x.device)
-    _check(_lib().hkg_mxfp4_code_bytes(rows, K), "hkg_mxfp4_code_bytes")
-    _check(_lib().hkg_mxfp4_code_bytes(K, rows), "hkg_mxfp4_code_bytes")
-    codes = on.empty((rows, _pad32(K) // 2), torch.uint8)
-    codes_t = on.empty((K, _pad32(rows) // 2), torch.uint8)
-    packed = on.bytes(_hkg.hkg_mx_packed_scale_bytes(rows, _pad32(K)))
-    packed_t = on.bytes(_hkg.hkg_mx_packed_scale_bytes(K, _pad32(rows)))
+    st = _handle(stream, x)
+    codes = _empty((rows, _pad32(K) >> 1), torch.uint8, x, stream)
+    codes_t = _empty((K, _pad32(rows) >> 1), torch.uint8, x, stream)
+    packed = _bytes(_scale_bytes(rows, K), x, stream)
+    packed_t = _bytes(_scale_bytes(K, rows), x, stream)
     _check(_lib().hkg_mxfp4_quantize_both(operand, operand_t, rows, K, px, xt, ld, codes.data_ptr(),
                                           packed.data_ptr(), codes_t.data_ptr(), packed_t.data_ptr(),
-                                          on.handle), "hkg_mxfp4_quantize_both")
+                                          st), "hkg_mxfp4_quantize_both")
     return codes, packed, codes_t, packed_t
 
 
@@ -193,11 +204,11 @@ def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     if K % 32:
         raise ValueError("codes must hold whole blocks of 32 (16 bytes a row)")
     pc, pp = _codes(codes, rows, K, "codes"), _packed(packed, rows, K, "packed")
-    on = _On(stream, codes.device)
+    st = _handle(stream, codes)
     dtype = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
-    out, po, ld = _output(on, out, (rows, K), dtype, "out")
+    out, po, ld = _output(out, (rows, K), dtype, "out", codes, stream)
     _check(_lib().hkg_mxfp4_dequantize(operand, rows, K, pc, pp, po, _elem_type(out, "out"), ld,
-                                       on.handle), "hkg_mxfp4_dequantize")
+                                       st), "hkg_mxfp4_dequantize")
     return out
 
 
@@ -211,14 +222,14 @@ def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
         raise ValueError("A and B must hold whole blocks of 32 (16 bytes a row)")
     pa, pb = _codes(A, M, K, "A"), _codes(B, N, K, "B")
     sa, sb = _packed(SA_packed, M, K, "SA_packed"), _packed(SB_packed, N, K, "SB_packed")
-    on = _On(stream, A.device)
-    C, pc, ldc = _output(on, C, (M, N), torch.bfloat16, "C")
+    st = _handle(stream, A)
+    C, pc, ldc = _output(C, (M, N), torch.bfloat16, "C", A, stream)
     pf = None
     if C_f32 is not None:
-        C_f32, pf, ldf = _output(on, C_f32, (M, N), torch.float32, "C_f32")
+        C_f32, pf, ldf = _output(C_f32, (M, N), torch.float32, "C_f32", A, stream)
         if ldf != ldc:
             raise ValueError("C and C_f32 must have the same row pitch")
-    _check(_lib().hkg_gemm_mxfp4(M, N, K, pa, pb, sa, sb, pc, pf, ldc, on.handle), "hkg_gemm_mxfp4")
+    _check(_lib().hkg_gemm_mxfp4(M, N, K, pa, pb, sa, sb, pc, pf, ldc, st), "hkg_gemm_mxfp4")
     return C
 
 
@@ -232,11 +243,11 @@ def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     M, K = x.shape
     N = W.shape[0]
     pw, ps = _codes(W, N, K, "W"), _packed(SW_packed, N, K, "SW_packed")
-    on = _On(stream, x.device)
-    y, py, ldy = _output(on, y, (M, N), torch.bfloat16, "y")
+    st = _handle(stream, x)
+    y, py, ldy = _output(y, (M, N), torch.bfloat16, "y", x, stream)
     need = _check(_lib().hkg_linear_mxfp4_workspace_bytes(M, N, K), "hkg_linear_mxfp4_workspace_bytes")
-    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
-    _check(_lib().hkg_linear_mxfp4(M, N, K, px, xt, ldx, pw, ps, py, ldy, pws, nws, on.handle),
+    workspace, pws, nws = _workspace(workspace, need, x, stream)
+    _check(_lib().hkg_linear_mxfp4(M, N, K, px, xt, ldx, pw, ps, py, ldy, pws, nws, st),
            "hkg_linear_mxfp4")
     return y
 
@@ -253,14 +264,14 @@ def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, 
     K = Wt.shape[0]
     pw, psw = _codes(Wt, K, N, "Wt"), _packed(SWt_packed, K, N, "SWt_packed")
     px, psx = _codes(Xt, K, M, "Xt"), _packed(SXt_packed, K, M, "SXt_packed")
-    on = _On(stream, dy.device)
-    dx, pdx, lddx = _output(on, dx, (M, K), torch.bfloat16, "dx")
-    dw, pdw, lddw = _output(on, dw, (N, K), torch.bfloat16, "dw")
+    st = _handle(stream, dy)
+    dx, pdx, lddx = _output(dx, (M, K), torch.bfloat16, "dx", dy, stream)
+    dw, pdw, lddw = _output(dw, (N, K), torch.bfloat16, "dw", dy, stream)
     need = _check(_lib().hkg_linear_mxfp4_backward_workspace_bytes(M, N, K),
                   "hkg_linear_mxfp4_backward_workspace_bytes")
-    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
+    workspace, pws, nws = _workspace(workspace, need, dy, stream)
     _check(_lib().hkg_linear_mxfp4_backward(M, N, K, pdy, t, lddy, pw, psw, px, psx, pdx, lddx, pdw,
-                                            lddw, pws, nws, on.handle), "hkg_linear_mxfp4_backward")
+                                            lddw, pws, nws, st), "hkg_linear_mxfp4_backward")
     return dx, dw
 
 
@@ -278,10 +289,10 @@ def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None
     pg, ldg = _hkg._matrix(G, "G")
     rows, cols = G.shape
     a, b, c = coefficients
-    on = _On(stream, G.device)
-    out, po, ldo = _output(on, out, (rows, cols), torch.bfloat16, "out")
+    st = _handle(stream, G)
+    out, po, ldo = _output(out, (rows, cols), torch.bfloat16, "out", G, stream)
     need = _check(_lib().hkg_orthogonalize_workspace_bytes(rows, cols), "hkg_orthogonalize_workspace_bytes")
-    workspace, pws, nws = _workspace(on, workspace, need, "workspace")
-    _check(_lib().hkg_orthogonalize(rows, cols, pg, t, ldg, steps, a, b, c, eps, po, ldo, pws, nws, on.handle),
+    workspace, pws, nws = _workspace(workspace, need, G, stream)
+    _check(_lib().hkg_orthogonalize(rows, cols, pg, t, ldg, steps, a, b, c, eps, po, ldo, pws, nws, st),
            "hkg_orthogonalize")
     return out
