@@ -9,67 +9,6 @@
 namespace hkg {
 namespace {
 
-// Rows row_off .. of tile (tm, tn) from one wave's blocks: a lane owns row 16 i + x
-// and, per pair of column blocks, 8 consecutive columns.  Whole tiles store 16 bytes
-// through one buffer resource, edge tiles check rows and columns.
-template <int kT, int kB>
-__device__ __forceinline__ void store_bf16(const Mx4GemmParams &p, int tm, int tn, int row_off, int col_off, int lane,
-                                           f32x4_t (&acc)[kB][kB])
-{
-    const int x = lane & 15, q = lane >> 4;
-    const int64_t row0 = (int64_t)tm * kT + row_off, col0 = (int64_t)tn * kT + col_off;
-    const bool vec = ((p.N | p.ldc) & 7) == 0;
-    const bool inside = (int64_t)(tm + 1) * kT <= p.M && (int64_t)(tn + 1) * kT <= p.N && vec;
-    if (inside && !p.C_f32 && (uint64_t)32 * kB * (uint64_t)p.ldc < (uint64_t(1) << 32)) {
-        const __amdgpu_buffer_rsrc_t rc = buffer_of(p.C + row0 * p.ldc + col0, (uint32_t)(32 * kB) * (uint32_t)p.ldc);
-        const int voff = (x * (int)p.ldc + 8 * q) * 2;
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-            const int soff = __builtin_amdgcn_readfirstlane((int)((uint32_t)(32 * i) * (uint32_t)p.ldc));
-            settle_row(acc, i);
-#pragma unroll
-            for (int h = 0; h < kB / 2; ++h) {
-                const f32x4_t lo = acc[i][2 * h], hi = acc[i][2 * h + 1];
-                const u32x4_t v = {pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]), pack2_bf16(hi[0], hi[1]),
-                                   pack2_bf16(hi[2], hi[3])};
-                __builtin_amdgcn_raw_buffer_store_b128(v, rc, voff + 64 * h, soff, 0);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-        const int64_t m = row0 + 16 * i + x;
-        settle_row(acc, i);
-        if (m >= p.M)
-            continue;
-#pragma unroll
-        for (int h = 0; h < kB / 2; ++h) {
-            const f32x4_t lo = acc[i][2 * h], hi = acc[i][2 * h + 1];
-            const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            const u32x4_t w = {pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]),
-                               pack2_bf16(v[6], v[7])};
-            const int64_t n = col0 + 32 * h + 8 * q, at = m * p.ldc + n;
-            if (vec && n < p.N) {
-                *reinterpret_cast<u32x4_t *>(p.C + at) = w;
-                if (p.C_f32) {
-                    *reinterpret_cast<f32x4_t *>(p.C_f32 + at) = lo;
-                    *reinterpret_cast<f32x4_t *>(p.C_f32 + at + 4) = hi;
-                }
-            } else if (!vec) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (n + e < p.N) {
-                        p.C[at + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                        if (p.C_f32)
-                            p.C_f32[at + e] = v[e];
-                    }
-                }
-            }
-        }
-    }
-}
-
 template <int kT>
 __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const TileOperands o, const Mx4GemmParams p)
 {
@@ -87,7 +26,36 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const 
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
     settle(acc);
-    store_bf16<kT>(p, tm, tn, loop.a_rows / kStepBytes, loop.b_rows / kStepBytes, loop.lane, acc);
+    // a lane owns row 16 i + x of block row i and, per pair of blocks, 8 consecutive columns
+    constexpr int kB = Loop::kB;
+    const int x = loop.lane & 15, q = loop.lane >> 4;
+    const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
+    barrier();   // every wave has read its last fragments
+    const Stage<kB> st(smem, loop.wave);
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+        settle_row(acc, i);
+#pragma unroll
+        for (int h = 0; h < kB / 2; ++h) {
+            const f32x4_t lo = acc[i][2 * h], hi = acc[i][2 * h + 1];
+            *st.unit(16 * i + x, 4 * h + q) = u32x4_t{pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]),
+                                                      pack2_bf16(hi[0], hi[1]), pack2_bf16(hi[2], hi[3])};
+        }
+    }
+    const int64_t at = row0 * p.ldc + col0;
+    store_stage(st, loop.lane, p.C + at, p.ldc, p.M - row0, p.N - col0, ((p.N | p.ldc) & 7) == 0 && p.ldc < (1 << 22));
+    if (!p.C_f32)
+        return;
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 16 * i + x, c = 32 * (j >> 1) + 8 * q + 4 * (j & 1) + e;
+                if (row0 + r < p.M && col0 + c < p.N)
+                    p.C_f32[at + r * p.ldc + c] = acc[i][j][e];
+            }
 }
 
 }  // namespace

@@ -489,6 +489,56 @@ __device__ __forceinline__ void settle_row(f32x4_t (&acc)[kB][kB], int i)
     }
 }
 
+// A wave's quarter of 16-bit results in LDS, so that stores go out as whole runs of
+// a row: straight from the accumulators, neighbouring lanes hold neighbouring rows
+// and every lane's 16 bytes are a request of their own (64 cycles a store; 32 stores
+// a wave took 8500 of a 256-tile's 57000 cycles at K = 4096 e2m1).  The units
+// of row r are permuted by its low bits (its bits above the first where two rows share
+// a bank line): 16 lanes with one unit of 16 rows, or with 16 neighbouring units, then
+// meet 16 different bank groups.
+template <int kB>
+struct Stage {
+    static constexpr int kSide = 16 * kB;
+    static constexpr int kPitch = kB == 4 ? 64 : 128;   // elements: a power of two of units
+    static constexpr int kUnits = kSide / 8;
+    uint16_t *base;
+
+    __device__ __forceinline__ Stage(char *smem, int wave) : base(reinterpret_cast<uint16_t *>(smem) + wave * kSide * kPitch) {}
+    __device__ __forceinline__ static int place(int row, int unit)
+    {
+        return row * kPitch + 8 * (unit ^ (kPitch == 128 ? row & 15 : (row >> 1) & 7));
+    }
+    __device__ __forceinline__ u32x4_t *unit(int row, int u) const
+    {
+        return reinterpret_cast<u32x4_t *>(base + place(row, u));
+    }
+};
+
+// Stores a staged quarter (rows x cols of it exist, at `to`, rows ld elements apart):
+// 16 lanes (8 or 12 of them for smaller tiles) write one row.  units: rows start
+// 16-byte aligned and cols is whole units, else element by element.
+template <int kB>
+__device__ __forceinline__ void store_stage(const Stage<kB> &st, int lane, uint16_t *to, int64_t ld, int rows, int cols,
+                                            bool units)
+{
+    constexpr int kUnits = Stage<kB>::kUnits, kSide = Stage<kB>::kSide;
+    rows = min(rows, kSide);
+    const __amdgpu_buffer_rsrc_t rs = buffer_of(to, units && rows > 0 ? (uint32_t)rows * (uint32_t)(2 * ld) : 0u);
+#pragma unroll 8
+    for (int k = 0; k < kSide * kUnits / 64; ++k) {
+        const int at = 64 * k + lane, row = at / kUnits, u = at % kUnits;
+        const u32x4_t w = *st.unit(row, u);
+        if (units) {
+            __builtin_amdgcn_raw_buffer_store_b128(w, rs, 8 * u < cols ? (int)(2 * (row * ld + 8 * u)) : kPastEnd, 0, 0);
+        } else if (row < rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * u + e < cols)
+                    to[row * ld + 8 * u + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
 // The tile of workgroup b of a triangle of Gm x Gm tiles, tm <= tn: consecutive
 // workgroups of an XCD (b mod 8 equal) take neighbouring tiles of one column, so
 // that its L2 holds that column's panel and a run of row panels.
