@@ -128,11 +128,9 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
 }
 
 // ---- a product of a step -----------------------------------------------------
-// v = alpha acc + beta D, stored as rows (straight) and/or as columns (transposed).
-// Columns are stored through LDS: a wave writes its rows there as 16-byte units,
-// unit u of row r in place u ^ r ^ (r >> 3) (so that neither the row writes nor the
-// column reads below share a bank), and reads 8 rows of a column back for each
-// 16-byte store of 8 consecutive elements.
+// v = alpha acc + beta D, stored as rows (straight) and/or as columns (transposed),
+// both through a staged quarter of the tile (tile16.h): D is loaded into it, each
+// lane replaces D's units by its results, and whole runs of rows or of columns leave.
 template <bool kBf16>
 __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
 {
@@ -149,22 +147,13 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
     return w;
 }
 
-// The first n of 8 elements, one by one (a result whose rows are not whole units).
-__device__ __forceinline__ void store_part(uint16_t *p, const u32x4_t &v, int n)
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n)
-            p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-}
-
 template <int kT, bool kBf16>
 __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(const TileOperands o, const OrthEpilogue p)
 {
     using Loop = TileLoop<F16, kT>;
-    constexpr int kB = Loop::kB, kSide = 16 * kB;   // a wave's quarter: kSide x kSide
-    constexpr int kPitch = kB == 4 ? 64 : 128;      // its rows in LDS: a power of two of units
-    static_assert(4 * kSide * kPitch * 2 <= Loop::kLds, "the four quarters fit the ring");
+    constexpr int kB = Loop::kB;
+    using St = Stage<kB>;
+    static_assert(4 * St::kSide * St::kPitch * 2 <= Loop::kLds, "the four quarters fit the ring");
     __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
     int tm, tn;
     if (o.triangle)
@@ -181,82 +170,73 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
     settle(acc);
-    const int x = loop.lane & 15, q = loop.lane >> 4;
+    const int lane = loop.lane, x = lane & 15, q = lane >> 4;
     const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
-    const bool columns = p.transposed && !(o.triangle && tm == tn && p.straight);
-    // Buffers over the wave's rows of D and of the straight result: rows past the
-    // matrix read zeros and drop stores, as do column units past it (lane offset
-    // kPastEnd), so nothing below branches.
-    const int rows = o.rows_a - row0;
-    auto over = [&](const void *base, int64_t ld) {
-        return buffer_of(static_cast<const uint16_t *>(base) + row0 * ld + col0,
-                         base && rows > 0 ? (uint32_t)min(rows, kSide) * (uint32_t)(2 * ld) : 0u);
-    };
-    auto lane_off = [&](int h, int64_t ld, int cols) {
-        return col0 + 32 * h + 8 * q < cols ? (int)(2 * (x * ld + 32 * h + 8 * q)) : kPastEnd;
-    };
-    auto row_off = [&](int i, int64_t ld) { return __builtin_amdgcn_readfirstlane((int)(32 * i * ld)); };
-    // D's part of the tile, all of it at once: the fragments' registers are free
-    u32x4_t d[kB][kB / 2];
-    const __amdgpu_buffer_rsrc_t rd = over(p.D, p.ldd);
+    const int rows = o.rows_a - row0, cols = o.rows_b - col0;   // of the quarter that exist
+    barrier();   // every wave has read its last fragments
+    const St st(smem, loop.wave);
+    constexpr int kSlots = St::kPitch / 8;   // units a staged row has room for
+    if (p.D) {
+        // rows and columns past D read zeros
+        const __amdgpu_buffer_rsrc_t rd =
+            buffer_of(p.D + row0 * p.ldd + col0, rows > 0 ? (uint32_t)min(rows, St::kSide) * (uint32_t)(2 * p.ldd) : 0u);
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
-#pragma unroll
-        for (int h = 0; h < kB / 2; ++h)
-            d[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rd, lane_off(h, p.ldd, (int)p.ldd), row_off(i, p.ldd), 0);
-    if (columns)
-        barrier();   // every wave has read its last fragments
-    uint16_t *lds = reinterpret_cast<uint16_t *>(smem) + loop.wave * kSide * kPitch;
-    // whole 16-byte units in 16-byte aligned rows (always so in the workspace)
-    const bool units_s = ((reinterpret_cast<uintptr_t>(p.straight) | (uintptr_t)(2 * p.lds) | (uintptr_t)(2 * p.cols_s)) & 15) == 0 &&
-                         p.lds < (1 << 22);
-    const bool units_t = ((reinterpret_cast<uintptr_t>(p.transposed) | (uintptr_t)(2 * p.ldt) | (uintptr_t)(2 * p.cols_t)) & 15) == 0 &&
-                         p.ldt < (1 << 22);
-    const __amdgpu_buffer_rsrc_t rs = over(units_s ? p.straight : nullptr, p.lds);
+        for (int k = 0; k < St::kSide * kSlots / 64; ++k) {
+            const int at = 64 * k + lane, row = at / kSlots;
+            const int u = (St::place(row, at % kSlots) - row * St::kPitch) / 8;   // the permutation is its own inverse
+            const bool in = u < St::kUnits && col0 + 8 * u < p.ldd;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rd, (__attribute__((address_space(3))) void *)(st.base + 512 * k), 16,
+                in ? (int)(2 * (row * p.ldd + 8 * u)) : kPastEnd, 0, 0, 0);
+        }
+        wait_loads<0>();
+    }
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
-        const int rl = 16 * i + x;
         settle_row(acc, i);
 #pragma unroll
         for (int h = 0; h < kB / 2; ++h) {
-            const int cl = 32 * h + 8 * q;
-            const f16x8_t dv = __builtin_bit_cast(f16x8_t, d[i][h]);
+            u32x4_t *w = st.unit(16 * i + x, 4 * h + q);
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[e] = p.alpha * acc[i][2 * h + (e >> 2)][e & 3] + p.beta * (float)dv[e];
-            const u32x4_t w = pack8<kBf16>(v);
-            if (units_s)
-                __builtin_amdgcn_raw_buffer_store_b128(w, rs, lane_off(h, p.lds, p.cols_s), row_off(i, p.lds), 0);
-            else if (p.straight && rl < rows)
-                store_part(p.straight + (row0 + rl) * p.lds + col0 + cl, w, p.cols_s - col0 - cl);
-            if (columns)
-                *reinterpret_cast<u32x4_t *>(lds + rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1))) = w;
+                v[e] = p.alpha * acc[i][2 * h + (e >> 2)][e & 3];
+            if (p.D) {
+                const f16x8_t d = __builtin_bit_cast(f16x8_t, *w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += p.beta * (float)d[e];
+            }
+            *w = pack8<kBf16>(v);
         }
     }
-    if (!columns)
+    if (p.straight)
+        store_stage(st, lane, p.straight + row0 * p.lds + col0, p.lds, rows, p.cols_s - col0,
+                    ((reinterpret_cast<uintptr_t>(p.straight) | (uintptr_t)(2 * p.lds) | (uintptr_t)(2 * p.cols_s)) & 15) == 0 &&
+                        p.lds < (1 << 22));
+    if (!p.transposed || (o.triangle && tm == tn))
         return;
-    wait_lds();   // the region is this wave's own
-    constexpr int kUnits = kSide / 8;   // 8-row units of a column
-    const int tcols = o.rows_b - col0;  // columns of the tile that exist: rows of the transposed result
+    const bool units = ((reinterpret_cast<uintptr_t>(p.transposed) | (uintptr_t)(2 * p.ldt) | (uintptr_t)(2 * p.cols_t)) & 15) == 0 &&
+                       p.ldt < (1 << 22);
+    uint16_t *to = p.transposed + col0 * p.ldt + row0;
+    const int tcols = p.cols_t - row0;
     const __amdgpu_buffer_rsrc_t rt =
-        buffer_of(p.transposed + col0 * p.ldt + row0,
-                  units_t && tcols > 0 ? (uint32_t)min(tcols, kSide) * (uint32_t)(2 * p.ldt) : 0u);
+        buffer_of(to, units && cols > 0 ? (uint32_t)min(cols, St::kSide) * (uint32_t)(2 * p.ldt) : 0u);
 #pragma unroll 4
-    for (int k = loop.lane; k < kSide * kUnits; k += 64) {
-        const int u = k % kUnits, cl = k / kUnits;
+    for (int k = 0; k < St::kSide * St::kUnits / 64; ++k) {
+        const int at = 64 * k + lane, u = at % St::kUnits, c = at / St::kUnits;   // rows 8 u .. of column c
         u32x4_t w = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int rl = 8 * u + e;
-            const uint32_t t = lds[rl * kPitch + 8 * (((cl >> 3) ^ rl ^ (rl >> 3)) & (kPitch / 8 - 1)) + (cl & 7)];
-            w[e >> 1] |= t << (16 * (e & 1));
+        for (int e = 0; e < 8; ++e)
+            w[e >> 1] |= (uint32_t)st.base[St::place(8 * u + e, c >> 3) + (c & 7)] << (16 * (e & 1));
+        if (units) {
+            __builtin_amdgcn_raw_buffer_store_b128(w, rt, 8 * u < tcols ? (int)(2 * (c * p.ldt + 8 * u)) : kPastEnd, 0, 0);
+        } else if (c < cols) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * u + e < tcols)
+                    to[c * p.ldt + 8 * u + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
         }
-        if (units_t)
-            __builtin_amdgcn_raw_buffer_store_b128(
-                w, rt, row0 + 8 * u < p.cols_t ? (int)(2 * (cl * p.ldt + 8 * u)) : kPastEnd, 0, 0);
-        else if (cl < tcols)
-            store_part(p.transposed + (int64_t)(col0 + cl) * p.ldt + row0 + 8 * u, w, p.cols_t - row0 - 8 * u);
     }
 }
 

@@ -493,9 +493,8 @@ __device__ __forceinline__ void settle_row(f32x4_t (&acc)[kB][kB], int i)
 // a row: straight from the accumulators, neighbouring lanes hold neighbouring rows
 // and every lane's 16 bytes are a request of their own (64 cycles a store; 32 stores
 // a wave took 8500 of a 256-tile's 57000 cycles at K = 4096 e2m1).  The units
-// of row r are permuted by its low bits (its bits above the first where two rows share
-// a bank line): 16 lanes with one unit of 16 rows, or with 16 neighbouring units, then
-// meet 16 different bank groups.
+// of a row are permuted (place) so that 16 lanes with one unit of 16 rows, with 16
+// neighbouring units, or with one element of every eighth row meet different banks.
 template <int kB>
 struct Stage {
     static constexpr int kSide = 16 * kB;
@@ -506,7 +505,7 @@ struct Stage {
     __device__ __forceinline__ Stage(char *smem, int wave) : base(reinterpret_cast<uint16_t *>(smem) + wave * kSide * kPitch) {}
     __device__ __forceinline__ static int place(int row, int unit)
     {
-        return row * kPitch + 8 * (unit ^ (kPitch == 128 ? row & 15 : (row >> 1) & 7));
+        return row * kPitch + 8 * (unit ^ (kPitch == 128 ? (row ^ (row >> 3)) & 15 : ((row >> 1) ^ (row >> 4)) & 7));
     }
     __device__ __forceinline__ u32x4_t *unit(int row, int u) const
     {
