@@ -20,6 +20,13 @@ constexpr int kMxStepScales = 512;    // scale bytes of one step of one group
 constexpr uint32_t kScaleOne = 127;   // E8M0 codes
 constexpr uint32_t kScaleNan = 255;
 
+// A buffer of `bytes` bytes: loads past it give zeros, stores past it are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
+}
+constexpr int kPastEnd = int(0x80000000u);       // a lane offset outside any buffer
+
 // Byte of the scale of (row r of a 128-row group, block b of a 128-k step)
 // inside the step's 512: 8 (16 b + x) + e, where fragment e gives lane x row r.
 // Operand A: r = 16 e + x.  Operand B: r = 32 (e >> 1) + 4 (e & 1) + (x & 3) +

@@ -168,93 +168,224 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams
     }
 }
 
-// ---- the product, operands read straight from memory ------------------------
-// One workgroup computes 16 rows (of A or x) x 32 columns (rows of B); its
-// waves take every kWaves-th 128-k step and add their sums in LDS.  B is the
-// matrix instruction's first operand: fragments 2 j and 2 j + 1 of a packed
-// group then give a lane 8 consecutive columns of one row of C, one 16-byte
-// store.  kXt: -1 A is codes, 0 / 1 x is bf16 / fp32 and each lane quantises
-// the one block that its fragment holds (16 q + x holds row x, block q), so the
-// quantised activations never leave the registers.
-constexpr int kDirectWaves = 4;
+// ---- the product of few rows ------------------------------------------------
+// What bounds it is reading B once, so each wave streams its own part of K and keeps
+// a whole run of loads in flight.  One workgroup computes 16 kMb rows (of A or x) x 32
+// columns (rows of B); its 8 waves take runs of kS 128-k steps in turn:
+//   wait for the run in LDS, take its fragments into registers, send the next run's
+//   loads into the same LDS, and multiply while they fly;
+// the waves' sums are joined in LDS at the end, in a fixed order.  The detour through
+// LDS is what makes the loads whole lines: a lane of a fragment holds 16 bytes of a row
+// of its own, and loaded straight into registers every lane is a request of its own
+// (16 x 8192 x 8192: 15.4 us so, x among them, against .. through LDS).
+// B is the matrix instruction's first operand: fragments 2 j and 2 j + 1 of a packed
+// group then give a lane 8 consecutive columns of one row of C.  kXt: -1 A is codes, 0
+// / 1 x is bf16 / fp32 and each lane quantises the one block that its fragment holds (16
+// q + x holds row x, block q), so the quantised activations never leave the registers.
+constexpr int kFewWaves = 8;
 
-template <int kXt>
-__global__ __launch_bounds__(64 * kDirectWaves) void mx4_direct_kernel(const Mx4GemmParams p)
+// kXt: see above.  kMb: 16-row blocks of A.  kS: steps of a run -- two where a compute
+// unit gets one workgroup, so that enough is in flight, else one, so that several
+// workgroups share it.
+template <int kXt, int kMb, int kS>
+struct FewRows {
+    static_assert(kXt < 0 || kMb == 1, "x is quantised for 16 rows");
+    static constexpr int kElem = kXt == 1 ? 4 : 2;
+    static constexpr int kRow = 64 * kS;                        // bytes of a row of codes in a run
+    static constexpr int kXRow = 128 * kElem;                   // bytes of a row of x in a step
+    static constexpr int kBBytes = 32 * kRow;
+    static constexpr int kABytes = kXt < 0 ? 16 * kMb * kRow : kS * 16 * kXRow;
+    static constexpr int kWave = kBBytes + kABytes;             // LDS bytes of one wave
+    static constexpr int kSums = kFewWaves * 64 * 9 * 4;
+    static constexpr int kLds = kFewWaves * kWave > kSums ? kFewWaves * kWave : kSums;
+
+    // Places of a row's 16-byte chunks in LDS, permuted so that the 16 rows of a
+    // fragment, which differ in bits 0, 1 and 3, 4 (B, interleaved) or 0..3 (A, x),
+    // fall into different 16-byte slots of the 256-byte bank line.
+    __device__ __forceinline__ static int b_chunk(int row, int c)
+    {
+        return kS == 2 ? c ^ (((row >> 1) & 1) | (((row >> 3) & 3) << 1)) : c ^ ((row >> 3) & 3);
+    }
+    __device__ __forceinline__ static int a_chunk(int row, int c)
+    {
+        return kS == 2 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
+    }
+    __device__ __forceinline__ static int x_chunk(int row, int c) { return c ^ (row & 15); }
+};
+
+template <int kXt, int kMb, int kS>
+__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(const Mx4GemmParams p)
 {
-    __shared__ float part[kDirectWaves][64][9];   // 9: neighbours' rows fall into other banks
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    using G = FewRows<kXt, kMb, kS>;
+    __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, q = lane >> 4;
-    const int n0 = 32 * blockIdx.x, m = 16 * blockIdx.y + x;
+    const int gn = (p.N + 31) / 32;
+    const int n0 = 32 * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
     const int nk = (p.kb + 63) / 64;              // 128-k steps
     const int g = n0 >> 7, j = (n0 >> 5) & 3;     // B's packed group, pair of fragments in it
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    const int rb = n0 + (x & 3) + 8 * (x >> 2);
-    const bool vec = ((reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.ldx * (kXt == 1 ? 4 : 2))) & 15) == 0;
-    for (int t = wave; t < nk; t += kDirectWaves) {
-        const int cb = 64 * t + 16 * q;           // byte of this lane's block in a row
-        const bool in = cb < p.kb;
-        u32x4_t b[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, a = {0, 0, 0, 0};
-        uint32_t sb = 0x7f7f, sa = kScaleOne;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (in && rb + 4 * h < p.N)
-                b[h] = *reinterpret_cast<const u32x4_t *>(p.B + (int64_t)(rb + 4 * h) * p.kb + cb);
-        sb = *reinterpret_cast<const uint16_t *>(p.SB + ((int64_t)g * nk + t) * kMxStepScales + 8 * lane + 2 * j);
-        if constexpr (kXt < 0) {
-            if (in && m < p.M) {
-                a = *reinterpret_cast<const u32x4_t *>(p.A + (int64_t)m * p.kb + cb);
-                sa = p.SA[((int64_t)(m >> 7) * nk + t) * kMxStepScales + scale_byte(0, m & 127, q)];
-            }
-        } else {
-            Vec8<kXt> v[4];
-            uint32_t big = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = load8<kXt>(p.x, p.ldx, m, p.M, 2 * cb + 8 * i, p.K, vec);
-                big = max_u32(big, v[i].amax_bits());
-            }
-            sa = scale_code(big);
-            const float s = scale_operand(sa);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = sa == kScaleNan ? 0u : v[i].codes(s);
-        }
-        acc[0] = mma_f4<0, 0>(b[0], a, acc[0], sb, sa);
-        acc[1] = mma_f4<1, 0>(b[1], a, acc[1], sb, sa);
-    }
-    // the sums are complete here for every lane: nothing below may move a
-    // matrix instruction under a lane mask
-    asm volatile("" : "+v"(acc[0]), "+v"(acc[1]));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        part[wave][lane][r] = acc[0][r];
-        part[wave][lane][4 + r] = acc[1][r];
-    }
-    __syncthreads();
-    // 512 sums for 256 threads: thread -> lane tid / 4 of the fragments, columns 2 (tid & 3), +1
-    const int fl = threadIdx.x >> 2, c = 2 * (threadIdx.x & 3);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDirectWaves; ++w) {
-        s0 += part[w][fl][c];
-        s1 += part[w][fl][c + 1];
-    }
-    const int row = 16 * blockIdx.y + (fl & 15), col = n0 + 8 * (fl >> 4) + c;
-    if (row >= p.M || col >= p.N)
-        return;
-    const int64_t at = row * p.ldc + col;
-    const uint32_t two = pack2_bf16(s0, s1);
-    if (col + 1 < p.N && (p.ldc & 1) == 0) {
-        *reinterpret_cast<uint32_t *>(p.C + at) = two;
+    const uint32_t span = (uint32_t)nk * kMxStepScales;
+    char *const lb = smem + wave * G::kWave, *const la = lb + G::kBBytes;
+    const int rows = min(16 * kMb, p.M - m0);
+    // buffers over the workgroup's rows: rows past the matrix read zeros
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(p.B + (int64_t)n0 * p.kb, (uint32_t)min(32, p.N - n0) * (uint32_t)p.kb);
+    const __amdgpu_buffer_rsrc_t rsb = buffer_of(p.SB + (int64_t)g * span, span);
+    __amdgpu_buffer_rsrc_t ra, rsa;
+    // x in whole aligned blocks, its 16 rows within one buffer: else element by element
+    const bool whole = kXt >= 0 && (p.K & 31) == 0 && p.ldx < (1 << 24) &&
+                       ((reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.ldx * G::kElem)) & 15) == 0;
+    if constexpr (kXt < 0) {
+        ra = buffer_of(p.A + (int64_t)m0 * p.kb, (uint32_t)rows * (uint32_t)p.kb);
+        rsa = buffer_of(p.SA + (int64_t)(m0 >> 7) * span, span);   // 16 kMb rows from m0 lie in one group
     } else {
-        p.C[at] = (uint16_t)two;
-        if (col + 1 < p.N)
-            p.C[at + 1] = (uint16_t)(two >> 16);
+        ra = buffer_of(static_cast<const char *>(p.x) + m0 * p.ldx * G::kElem,
+                       whole ? (uint32_t)((rows - 1) * p.ldx + p.K) * G::kElem : 0u);
     }
-    if (p.C_f32) {
-        p.C_f32[at] = s0;
-        if (col + 1 < p.N)
-            p.C_f32[at + 1] = s1;
+    auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, char *to, int voff) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)to, 16, voff, 0, 0, 0);
+    };
+    uint32_t sb[kS], sa[kS];
+    // the loads of run r (steps kS r ..)
+    auto send = [&](int r) {
+#pragma unroll
+        for (int u = 0; u < kS; ++u) {            // a step past the end has zeros, and a scale in range
+            const int ss = min(kS * r + u, nk - 1) * kMxStepScales;
+            sb[u] = __builtin_amdgcn_raw_buffer_load_b16(rsb, 8 * lane + 2 * j, ss, 0);
+            if constexpr (kXt < 0) {
+                if constexpr (kMb == 4)
+                    sa[u] = __builtin_amdgcn_raw_buffer_load_b32(rsa, 8 * lane + ((m0 >> 4) & 4), ss, 0);
+                else
+                    sa[u] = __builtin_amdgcn_raw_buffer_load_b8(rsa, 8 * lane + ((m0 >> 4) & 7), ss, 0);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < G::kBBytes / 1024; ++d) {
+            constexpr int kC = 4 * kS;            // chunks of a row
+            const int row = 64 / kC * d + lane / kC, at = G::kRow * r + 16 * G::b_chunk(row, lane % kC);
+            to_lds(rb, lb + 1024 * d, at < p.kb ? row * p.kb + at : kPastEnd);
+        }
+        if constexpr (kXt < 0) {
+#pragma unroll
+            for (int d = 0; d < G::kABytes / 1024; ++d) {
+                constexpr int kC = 4 * kS;
+                const int row = 64 / kC * d + lane / kC, at = G::kRow * r + 16 * G::a_chunk(row, lane % kC);
+                if (64 / kC * d < rows)           // rows past the matrix: whatever LDS holds, in columns not stored
+                    to_lds(ra, la + 1024 * d, at < p.kb ? row * p.kb + at : kPastEnd);
+            }
+        } else if (whole) {
+            constexpr int kChunks = G::kXRow / 16, kRows = 64 / kChunks;   // rows a load covers
+#pragma unroll
+            for (int u = 0; u < kS; ++u)
+#pragma unroll
+                for (int d = 0; d < 16 / kRows; ++d) {
+                    const int row = kRows * d + lane / kChunks, c = G::x_chunk(row, lane % kChunks);
+                    const int k = 128 * (kS * r + u) + 16 * c / G::kElem;
+                    if (kRows * d < rows)
+                        to_lds(ra, la + 1024 * (u * (16 / kRows) + d),
+                               k < p.K ? (int)(row * p.ldx + k) * G::kElem : kPastEnd);
+                }
+        }
+    };
+    f32x4_t acc[kMb][2];
+#pragma unroll
+    for (int i = 0; i < kMb; ++i)
+        acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int runs = (nk + kS - 1) / kS;
+    if (wave < runs)
+        send(wave);
+    for (int r = wave; r < runs; r += kFewWaves) {
+        u32x4_t b[kS][2], a[kS][kMb];
+        Vec8<(kXt < 0 ? 0 : kXt)> v[kS][4];
+        uint32_t sb_now[kS], sa_now[kS];
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const int br = (x & 3) + 8 * (x >> 2);
+#pragma unroll
+        for (int u = 0; u < kS; ++u) {
+            sb_now[u] = sb[u];
+            sa_now[u] = sa[u];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                b[u][h] = *reinterpret_cast<const u32x4_t *>(lb + G::kRow * (br + 4 * h) +
+                                                               16 * G::b_chunk(br + 4 * h, 4 * u + q));
+            if constexpr (kXt < 0) {
+#pragma unroll
+                for (int i = 0; i < kMb; ++i)
+                    a[u][i] = *reinterpret_cast<const u32x4_t *>(la + G::kRow * (16 * i + x) +
+                                                                   16 * G::a_chunk(x, 4 * u + q));
+            } else if (whole) {
+                constexpr int kVecs = kXt == 1 ? 2 : 1;   // 16-byte units of 8 elements
+#pragma unroll
+                for (int i = 0; i < 4 * kVecs; ++i) {
+                    const u32x4_t t = *reinterpret_cast<const u32x4_t *>(
+                        la + 16 * G::kXRow * u + G::kXRow * x + 16 * G::x_chunk(x, 4 * kVecs * q + i));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        v[u][i / kVecs].w[4 * (i % kVecs) + w] = t[w];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[u][i] = load8<(kXt < 0 ? 0 : kXt)>(p.x, p.ldx, m0 + x, p.M, 128 * (kS * r + u) + 32 * q + 8 * i, p.K, false);
+            }
+        }
+        // the fragments are in registers: their LDS is free
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (r + kFewWaves < runs)
+            send(r + kFewWaves);
+#pragma unroll
+        for (int u = 0; u < kS; ++u) {
+            if constexpr (kXt >= 0) {
+                uint32_t big = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    big = max_u32(big, v[u][i].amax_bits());
+                sa_now[u] = scale_code(big);
+                const float s = scale_operand(sa_now[u]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a[u][0][i] = sa_now[u] == kScaleNan ? 0u : v[u][i].codes(s);
+            }
+            acc[0][0] = mma_f4<0, 0>(b[u][0], a[u][0], acc[0][0], sb_now[u], sa_now[u]);
+            acc[0][1] = mma_f4<1, 0>(b[u][1], a[u][0], acc[0][1], sb_now[u], sa_now[u]);
+            if constexpr (kMb == 4) {
+                acc[1][0] = mma_f4<0, 1>(b[u][0], a[u][1], acc[1][0], sb_now[u], sa_now[u]);
+                acc[1][1] = mma_f4<1, 1>(b[u][1], a[u][1], acc[1][1], sb_now[u], sa_now[u]);
+                acc[2][0] = mma_f4<0, 2>(b[u][0], a[u][2], acc[2][0], sb_now[u], sa_now[u]);
+                acc[2][1] = mma_f4<1, 2>(b[u][1], a[u][2], acc[2][1], sb_now[u], sa_now[u]);
+                acc[3][0] = mma_f4<0, 3>(b[u][0], a[u][3], acc[3][0], sb_now[u], sa_now[u]);
+                acc[3][1] = mma_f4<1, 3>(b[u][1], a[u][3], acc[3][1], sb_now[u], sa_now[u]);
+            }
+        }
+    }
+    float(*part)[64][9] = reinterpret_cast<float(*)[64][9]>(smem);   // 9: neighbours' rows fall into other banks
+#pragma unroll
+    for (int i = 0; i < kMb; ++i) {
+        // the sums are complete here for every lane: nothing below may move a
+        // matrix instruction under a lane mask
+        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]));
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            part[wave][lane][r] = acc[i][0][r];
+            part[wave][lane][4 + r] = acc[i][1][r];
+        }
+        __syncthreads();
+        // 16 x 32 results: lane 16 (c / 8) + r of the fragments holds row r, column c
+#pragma unroll
+        for (int o = threadIdx.x; o < 512; o += 64 * kFewWaves) {
+            const int r = o >> 5, c = o & 31;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w)
+                s += part[w][16 * (c >> 3) + r][c & 7];
+            const int row = m0 + 16 * i + r, col = n0 + c;
+            if (row < p.M && col < p.N) {
+                const int64_t at = row * p.ldc + col;
+                p.C[at] = (uint16_t)pack2_bf16(s, 0.f);
+                if (p.C_f32)
+                    p.C_f32[at] = s;
+            }
+        }
     }
 }
 
@@ -287,16 +418,29 @@ hipError_t launch_mx4_dequantize(ElemType t, const DequantParams &p, hipStream_t
     return hipGetLastError();
 }
 
-hipError_t launch_mx4_direct(ElemType xt, const Mx4GemmParams &p, hipStream_t stream)
+template <int kXt, int kMb, int kS>
+static hipError_t few_rows(const Mx4GemmParams &p, unsigned blocks, hipStream_t stream)
 {
-    const dim3 grid((p.N + 31) / 32, (p.M + 15) / 16), block(64 * kDirectWaves);
-    if (p.A)
-        hipLaunchKernelGGL(mx4_direct_kernel<-1>, grid, block, 0, stream, p);
-    else if (xt == kElemBf16)
-        hipLaunchKernelGGL(mx4_direct_kernel<0>, grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL(mx4_direct_kernel<1>, grid, block, 0, stream, p);
+    hipLaunchKernelGGL((mx4_few_rows_kernel<kXt, kMb, kS>), dim3(blocks), dim3(64 * kFewWaves), 0, stream, p);
     return hipGetLastError();
+}
+
+hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream)
+{
+    const int mb = p.A && p.M > 16 ? 4 : 1;
+    const unsigned blocks = (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
+    // two-step runs (96 KiB of LDS) where each of 256 compute units has at most one
+    // workgroup, or for a long K: 256 x 4096 x 14336 24.4 us against 27.1 in one-step
+    // runs, which let three workgroups share a unit (256 x 4096 x 4096: 9.3 against 10.5)
+    const bool two = blocks <= 256 || p.K >= 8192;
+    if (p.A) {
+        if (mb == 1)   // 48 KiB in two-step runs
+            return few_rows<-1, 1, 2>(p, blocks, stream);
+        return two ? few_rows<-1, 4, 2>(p, blocks, stream) : few_rows<-1, 4, 1>(p, blocks, stream);
+    }
+    if (xt == kElemF32)   // 80 KiB in one-step runs
+        return few_rows<1, 1, 1>(p, blocks, stream);
+    return two ? few_rows<0, 1, 2>(p, blocks, stream) : few_rows<0, 1, 1>(p, blocks, stream);
 }
 
 }  // namespace hkg

@@ -90,14 +90,25 @@ hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const
     return p;
 }
 
+// The product of two MXFP4 matrices: up to 512 blocks of 64 x 32 results (two for each
+// compute unit) the kernel for few rows, which splits K over a workgroup's waves; above,
+// tiles, which read each operand fewer times.  Measured at 512 blocks: 256 x 4096 x 4096
+// 9.3 us against 10.7 on 128-tiles, 512 x 2048 x 2048 6.3 against 7.2, 256 x 4096 x 14336
+// 24.4 against 35.8; at 896 and 1024: 128 x 14336 x 4096 17.6 against 13.4, 256 x 8192 x
+// 8192 34.5 against 23.2.
 hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 {
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
+        return hkg::launch_mx4_few_rows(hkg::kElemBf16, p, st);
     const int tile = ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128 ? 128 : 256;
-    return hkg::launch_mx4_tiles(tile, order_of(p.M, p.N, p.kb, tile), p, static_cast<hipStream_t>(stream));
+    return hkg::launch_mx4_tiles(tile, order_of(p.M, p.N, p.kb, tile), p, st);
 }
 
-// Rows of x up to which the linear layer quantises inside the product.
-constexpr int64_t kFusedRows = 16;
+// Whether the linear layer quantises x inside the product: up to 16 rows, whose part of
+// the work each workgroup then repeats, while that costs less than a launch of its own
+// (16 x 4096 x 14336: 14.1 us against 8.1 + 4; 16 x 8192 x 8192: 11.3 against 9.3 + 4).
+bool fused_linear(int64_t M, int64_t K) { return M <= 16 && K <= 10240; }
 
 }  // namespace
 }  // namespace hkg::api
@@ -192,7 +203,7 @@ int64_t hkg_linear_mxfp4_workspace_bytes(int64_t M, int64_t N, int64_t K)
         return HKG_ERR_SHAPE;
     if (!mx4_fits(M, K) || !mx4_fits(N, K))
         return HKG_ERR_SIZE;
-    return M <= kFusedRows || N == 0 ? 0 : round16(mx4_codes(M, K)) + mx4_scales(M, K);
+    return fused_linear(M, K) || N == 0 ? 0 : round16(mx4_codes(M, K)) + mx4_scales(M, K);
 }
 
 int hkg_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void *x, int32_t x_type, int64_t ldx,
@@ -237,7 +248,7 @@ int hkg_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void *x, int32_t x_t
         hkg::Mx4GemmParams p = product(M, N, K, nullptr, nullptr, W, SW, y, nullptr, ldy);
         p.x = x;
         p.ldx = ldx;
-        return launched(hkg::launch_mx4_direct(t, p, st));
+        return launched(hkg::launch_mx4_few_rows(t, p, st));
     }
     uint8_t *codes = static_cast<uint8_t *>(workspace), *packed = codes + round16(mx4_codes(M, K));
     const hkg::QuantParams q = {x, ldx, static_cast<int>(M), static_cast<int>(K), HKG_MX_OPERAND_A,

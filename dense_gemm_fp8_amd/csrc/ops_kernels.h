@@ -42,7 +42,7 @@ struct Mx4GemmParams {
     int64_t ldc;
     int M, N, K, kb;
 };
-hipError_t launch_mx4_direct(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
+hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
 
 // A grid of Gm x Gn tiles and the order its workgroups walk it in (remap.h).
 struct TileOrder {

@@ -41,7 +41,6 @@ namespace hkg {
 
 constexpr int kStepBytes = 128;                  // one K step of one row
 constexpr int kLoadBytes = 1024;                 // one wave-wide load to LDS: 8 rows
-constexpr int kPastEnd = int(0x80000000u);       // a lane offset outside any buffer
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
@@ -92,10 +91,6 @@ __device__ __forceinline__ int copy_s(int x)
     return y;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
-}
 // From a panel's first row to the last of its `rows` rows' kb bytes: what lies
 // past them reads as zeros.
 __device__ __forceinline__ uint32_t panel_range(int rows, int pitch, int kb)

@@ -89,8 +89,8 @@ int hkg_gemm_mxfp4(int64_t M, int64_t N, int64_t K, const void *A, const void *B
 /*
  * A linear layer with MXFP4 weights: y[M][N] = bf16(Q(x)[M][K] * W[N][K]^T),
  * Q the quantisation above.  The same result as hkg_mxfp4_quantize followed by
- * hkg_gemm_mxfp4 up to the order of the fp32 sums; up to 16 rows x is
- * quantised inside the product (one launch, no workspace used).
+ * hkg_gemm_mxfp4 up to the order of the fp32 sums; up to 16 rows of
+ * K <= 10240 x is quantised inside the product (one launch, no workspace used).
  *   x  bf16 or fp32 (x_type), W / SW codes and packed scales (operand B)
  *   y  bf16, rows ldy elements apart (0 = N)
  */
