@@ -101,8 +101,25 @@ hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
         return hkg::launch_mx4_few_rows(hkg::kElemBf16, p, st);
-    const int tile = ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128 ? 128 : 256;
-    return hkg::launch_mx4_tiles(tile, order_of(p.M, p.N, p.kb, tile), p, st);
+    if (ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128)
+        return hkg::launch_mx4_tiles(128, order_of(p.M, p.N, p.kb, 128), p, st);
+    const TileSplit split = split_last_round(p.M, p.N);
+    hkg::Mx4GemmParams head = p, rest = p;
+    if (split.keep > 0) {
+        // a multiple of 256 rows or columns: whole groups of packed scales
+        const int64_t packed = mx_packed_bytes(split.keep, 2 * (int64_t)p.kb), codes = split.keep * p.kb;
+        const int64_t at = split.by_rows ? split.keep * p.ldc : split.keep;
+        (split.by_rows ? head.M : head.N) = static_cast<int>(split.keep);
+        (split.by_rows ? rest.M : rest.N) -= static_cast<int>(split.keep);
+        (split.by_rows ? rest.A : rest.B) += codes;
+        (split.by_rows ? rest.SA : rest.SB) += packed;
+        rest.C += at;
+        rest.C_f32 += rest.C_f32 ? at : 0;
+    }
+    const hipError_t e = hkg::launch_mx4_tiles(256, order_of(head.M, head.N, p.kb, 256), head, st);
+    if (e != hipSuccess || split.keep == 0)
+        return e;
+    return hkg::launch_mx4_tiles(128, order_of(rest.M, rest.N, p.kb, 128), rest, st);
 }
 
 // Whether the linear layer quantises x inside the product: up to 16 rows, whose part of

@@ -50,20 +50,57 @@ bool sizes_fit(int64_t rows, int64_t cols)
 // The tile of a product (M x N, or the triangle of an M x M): the one whose rounds
 // of the 256 compute units take least, a unit's time for a tile growing with its
 // area and, for smaller tiles, with the LDS bytes per matrix instruction (two
-// 128-tiles share a compute unit).
+// 128-tiles share a compute unit).  256-tiles are priced with their last round
+// split off (split_last_round), where that is done.
 int pick_tile(int64_t M, int64_t N, bool triangle)
 {
     int best = 256;
     double least = 0.0;
     for (const int t : {256, 192, 128}) {
         const int64_t gm = ceil_div(M, t), gn = ceil_div(N, t), tiles = triangle ? gm * (gm + 1) / 2 : gm * gn;
-        const double cost = (double)ceil_div(tiles, 256) * t * t * (t == 256 ? 1.0 : t == 192 ? 1.05 : 1.2);
+        double cost = (double)ceil_div(tiles, 256) * t * t * (t == 256 ? 1.0 : t == 192 ? 1.05 : 1.2);
+        if (t == 256 && !triangle && split_last_round(M, N).keep > 0)
+            cost = (double)(tiles / 256 + 0.78) * t * t;
         if (least == 0.0 || cost < least) {
             least = cost;
             best = t;
         }
     }
     return best;
+}
+
+// X <- a X + P X (m x n), whole or in the two parts of split_last_round.
+hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpilogue &e, hipStream_t stream)
+{
+    const TileSplit split = tile == 256 ? split_last_round(p.M, p.N) : TileSplit{0, false};
+    if (split.keep == 0)
+        return hkg::launch_orth_product(tile, order_of(p.M, p.N, 2 * p.K, tile), false, p, e, stream);
+    hkg::OrthProduct head = p, rest = p;
+    hkg::OrthEpilogue re = e;
+    const int keep = static_cast<int>(split.keep);
+    const int64_t skip = 2 * (int64_t)keep * p.K;   // bytes of its operand rows
+    if (split.by_rows) {
+        head.M = keep;
+        rest.M -= keep;
+        rest.A = static_cast<const char *>(p.A) + skip;
+        re.D += keep * e.ldd;
+        re.straight += e.straight ? keep * e.lds : 0;
+        re.transposed += e.transposed ? keep : 0;
+        re.cols_t -= keep;
+    } else {
+        head.N = keep;
+        rest.N -= keep;
+        rest.B = static_cast<const char *>(p.B) + skip;
+        re.D += keep;
+        re.straight += e.straight ? keep : 0;
+        re.cols_s -= keep;
+        re.cols_d -= keep;
+        re.transposed += e.transposed ? keep * e.ldt : 0;
+    }
+    const hipError_t err = hkg::launch_orth_product(256, order_of(head.M, head.N, 2 * p.K, 256), false, head, e, stream);
+    if (err != hipSuccess)
+        return err;
+    return hkg::launch_orth_product(128, order_of(rest.M, rest.N, 2 * p.K, 128), false, rest, re, stream);
 }
 
 }  // namespace
@@ -146,16 +183,16 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
         const _Float16 *x16 = reinterpret_cast<const _Float16 *>(x);
         // A = X X^T
         rc = launched(hkg::launch_orth_product(sym, order_of(m, m, 2 * np, sym), true, {x, x, m, m, np},
-                                               {s, 0.0f, nullptr, 0, am, mp, mp, am, mp, mp, 0}, st));
+                                               {s, 0.0f, nullptr, 0, 0, am, mp, mp, am, mp, mp, 0}, st));
         // P = b A + c A A
         if (rc == HKG_OK)
             rc = launched(hkg::launch_orth_product(
                 sym, order_of(m, m, 2 * mp, sym), true, {am, am, m, m, mp},
-                {c * s, b, reinterpret_cast<const _Float16 *>(am), mp, pm, mp, mp, pm, mp, mp, 0}, st));
+                {c * s, b, reinterpret_cast<const _Float16 *>(am), mp, mp, pm, mp, mp, pm, mp, mp, 0}, st));
         // X <- a X + P X, as X and X^T, or the result in its own orientation
-        hkg::OrthEpilogue ep = {s, a, x16, np, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
+        hkg::OrthEpilogue ep = {s, a, x16, np, np, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
         if (last) {
-            ep = {s * s, a * s, x16, np, nullptr, 0, 0, nullptr, 0, 0, 1};
+            ep = {s * s, a * s, x16, np, np, nullptr, 0, 0, nullptr, 0, 0, 1};
             if (tall) {
                 ep.transposed = static_cast<uint16_t *>(out);
                 ep.ldt = ldo;
@@ -167,8 +204,7 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
             }
         }
         if (rc == HKG_OK)
-            rc = launched(hkg::launch_orth_product(upd, order_of(m, n, 2 * mp, upd), false,
-                                                   {pm, xt[i & 1], m, n, mp}, ep, st));
+            rc = launched(launch_update(upd, {pm, xt[i & 1], m, n, mp}, ep, st));
     }
     return rc;
 }

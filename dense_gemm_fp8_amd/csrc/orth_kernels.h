@@ -11,7 +11,8 @@
 namespace hkg {
 
 // X, X X^T and b A + c A A are held as fp16 times this.
-constexpr float kOrthScale = 4096.0f;
+constexpr int kOrthScaleLog2 = 12;
+constexpr float kOrthScale = 1 << kOrthScaleLog2;
 
 struct OrthInput {
     const void *G;       // [rows][cols], rows ldg elements apart
@@ -29,8 +30,9 @@ struct OrthProduct {
 // With a triangle of tiles both are the same symmetric matrix.
 struct OrthEpilogue {
     float alpha, beta;
-    const _Float16 *D;   // [M], rows ldd elements apart, or null
+    const _Float16 *D;   // [M], rows ldd elements apart, cols_d of each read, or null
     int64_t ldd;
+    int cols_d;
     uint16_t *straight;  // rows lds apart, cols_s columns of each are stored
     int64_t lds;
     int cols_s;

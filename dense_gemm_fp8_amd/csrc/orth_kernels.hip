@@ -22,26 +22,58 @@
 namespace hkg {
 namespace {
 
+// Element e of an 8-element group in fp32.
+template <int kElem>
+__device__ __forceinline__ float element(const Vec8<kElem> &v, int e)
+{
+    if constexpr (kElem == 0)
+        return __builtin_bit_cast(float, e & 1 ? v.w[e >> 1] & 0xffff0000u : v.w[e >> 1] << 16);
+    else
+        return __builtin_bit_cast(float, v.w[e]);
+}
+template <int kElem>
+__device__ __forceinline__ bool rows_aligned(const OrthInput &p)
+{
+    return ((reinterpret_cast<uintptr_t>(p.G) | (uintptr_t)(p.ldg * (kElem == 0 ? 2 : 4))) & 15) == 0;
+}
+
 // ---- |G|^2: partial sums in 64 bits, joined in a fixed order -----------------
+// (64 bits because squares of fp32 values leave fp32's range; reading G bounds it:
+// 117 MB of bf16 in .. us)
 template <int kElem>
 __global__ __launch_bounds__(256) void orth_norm_kernel(const OrthInput p, double *partial)
 {
     double s = 0.0;
-    const int64_t vecs = (p.cols + 7) / 8, total = vecs * p.rows;
-    const bool vec = (((reinterpret_cast<uintptr_t>(p.G)) | (uintptr_t)(p.ldg * (kElem == 0 ? 2 : 4))) & 15) == 0;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / vecs), col = 8 * (int)(i % vecs);
-        const Vec8<kElem> v = load8<kElem>(p.G, p.ldg, row, p.rows, col, p.cols, vec);
+    const bool vec = rows_aligned<kElem>(p);
+    // rows without gaps or tails are one long row
+    const bool flat = vec && p.ldg == p.cols && p.cols % 8 == 0;
+    const int64_t vecs = flat ? (int64_t)p.rows * (p.cols / 8) : (p.cols + 7) / 8;
+    const int64_t total = flat ? vecs : vecs * p.rows, stride = (int64_t)gridDim.x * 256;
+    constexpr int kU = 4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += kU * stride) {
+        Vec8<kElem> v[kU];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t b;
-            if constexpr (kElem == 0)
-                b = e & 1 ? v.w[e >> 1] & 0xffff0000u : v.w[e >> 1] << 16;
-            else
-                b = v.w[e];
-            const double f = (double)__builtin_bit_cast(float, b);
-            s += f * f;
+        for (int u = 0; u < kU; ++u) {
+            const int64_t k = i + u * stride;
+            if (flat) {
+                const u32x4_t *q = static_cast<const u32x4_t *>(p.G) + (k < total ? k : i) * (kElem == 0 ? 1 : 2);
+#pragma unroll
+                for (int h = 0; h < (kElem == 0 ? 1 : 2); ++h)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        v[u].w[4 * h + w] = q[h][w];
+            } else {
+                const int row = (int)(k / vecs), col = 8 * (int)(k % vecs);
+                v[u] = load8<kElem>(p.G, p.ldg, row, p.rows, col, p.cols, vec);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double f = (double)element<kElem>(v[u], e);
+                s += i + u * stride < total ? f * f : 0.0;
+            }
     }
     __shared__ double sums[256];
     sums[threadIdx.x] = s;
@@ -57,14 +89,22 @@ __global__ __launch_bounds__(256) void orth_norm_kernel(const OrthInput p, doubl
 
 // ---- X = G / (|G| + eps) in scaled fp16, and its transpose -------------------
 // A 64 x 64 tile a workgroup: rows x ps (straight) and cols x pt (transposed),
-// zeros past the matrix.  out: with no steps at all, the bf16 result itself.
+// zeros past the matrix.  out: with no steps at all, the bf16 result itself.  Bound
+// by its bytes: 14336 x 4096 bf16 reads 117 and writes 235 MB in .. us.
 template <int kElem>
 __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, const double *partial, int parts,
                                                            float eps, _Float16 *straight, int ps, _Float16 *transposed,
                                                            int pt, uint16_t *out, int64_t ldo)
 {
     __shared__ double sums[256];
-    __shared__ float tile[64][65];
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64 * 64];
+    const int tc = (p.cols + 63) / 64, r0 = blockIdx.x / tc * 64, c0 = blockIdx.x % tc * 64;
+    const bool vec = rows_aligned<kElem>(p);
+    const int rl = threadIdx.x >> 3, u = threadIdx.x & 7;   // rows rl and rl + 32, unit of 8 columns
+    Vec8<kElem> v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        v[h] = load8<kElem>(p.G, p.ldg, r0 + rl + 32 * h, p.rows, c0 + 8 * u, p.cols, vec);
     double s = 0.0;
     for (int i = threadIdx.x; i < parts; i += 256)
         s += partial[i];
@@ -77,30 +117,18 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
     }
     // a norm that is no number makes every element NaN; a zero matrix stays zero
     const double norm = sqrt(sums[0]);
-    const double inv = norm > 0.0 ? 1.0 / (norm + (double)eps) : 0.0;
-    const double mul = norm == 0.0 ? 0.0 : isfinite(norm) ? inv : (double)NAN;
-    const double scaled = mul * kOrthScale;
-    const int tc = (p.cols + 63) / 64, r0 = blockIdx.x / tc * 64, c0 = blockIdx.x % tc * 64;
-    const bool vec = (((reinterpret_cast<uintptr_t>(p.G)) | (uintptr_t)(p.ldg * (kElem == 0 ? 2 : 4))) & 15) == 0;
+    const double mul = norm == 0.0 ? 0.0 : isfinite(norm) ? 1.0 / (norm + (double)eps) : (double)NAN;
+    // mul as mantissa and exponent: G 2^exp is exact (the result is at most 1 in
+    // size), so one rounding in fp32 comes before fp16's, whatever the norm
+    int exp = 0;
+    const float mant = (float)frexp(mul, &exp);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int rl = (threadIdx.x >> 3) + 32 * h, cl = 8 * (threadIdx.x & 7);
-        const int row = r0 + rl, col = c0 + cl;
-        const Vec8<kElem> v = load8<kElem>(p.G, p.ldg, row, p.rows, col, p.cols, vec);
+        const int row = r0 + rl + 32 * h, col = c0 + 8 * u;
         f16x8_t x;
-        uint16_t y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t b;
-            if constexpr (kElem == 0)
-                b = e & 1 ? v.w[e >> 1] & 0xffff0000u : v.w[e >> 1] << 16;
-            else
-                b = v.w[e];
-            const double f = (double)__builtin_bit_cast(float, b);
-            x[e] = (_Float16)(float)(f * scaled);
-            tile[rl][cl + e] = (float)x[e];
-            y[e] = (uint16_t)pack2_bf16((float)(f * mul), 0.f);
-        }
+        for (int e = 0; e < 8; ++e)
+            x[e] = (_Float16)(ldexpf(element<kElem>(v[h], e), exp + kOrthScaleLog2) * mant);
         if (row < p.rows) {
             if (straight)
                 *reinterpret_cast<f16x8_t *>(straight + (int64_t)row * ps + col) = x;
@@ -108,22 +136,23 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (col + e < p.cols)
-                        out[row * ldo + col + e] = y[e];
+                        out[row * ldo + col + e] = (uint16_t)pack2_bf16(ldexpf(element<kElem>(v[h], e), exp) * mant, 0.f);
         }
+        *reinterpret_cast<f16x8_t *>(tile + Stage<4>::place(rl + 32 * h, u)) = x;
     }
     if (!transposed)
         return;
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int cl = (threadIdx.x >> 3) + 32 * h, rl = 8 * (threadIdx.x & 7);
-        if (c0 + cl >= p.cols)
+        const int c = rl + 32 * h;   // column c, rows 8 u .. + 7
+        if (c0 + c >= p.cols)
             continue;
-        f16x8_t x;
+        u32x4_t w = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            x[e] = (_Float16)tile[rl + e][cl];
-        *reinterpret_cast<f16x8_t *>(transposed + (int64_t)(c0 + cl) * pt + r0 + rl) = x;
+            w[e >> 1] |= (uint32_t)tile[Stage<4>::place(8 * u + e, c >> 3) + (c & 7)] << (16 * (e & 1));
+        *reinterpret_cast<u32x4_t *>(transposed + (int64_t)(c0 + c) * pt + r0 + 8 * u) = w;
     }
 }
 
@@ -184,7 +213,7 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
         for (int k = 0; k < St::kSide * kSlots / 64; ++k) {
             const int at = 64 * k + lane, row = at / kSlots;
             const int u = (St::place(row, at % kSlots) - row * St::kPitch) / 8;   // the permutation is its own inverse
-            const bool in = u < St::kUnits && col0 + 8 * u < p.ldd;
+            const bool in = u < St::kUnits && col0 + 8 * u < p.cols_d;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rd, (__attribute__((address_space(3))) void *)(st.base + 512 * k), 16,
                 in ? (int)(2 * (row * p.ldd + 8 * u)) : kPastEnd, 0, 0, 0);
@@ -242,7 +271,7 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
 
 }  // namespace
 
-constexpr int kNormParts = 512;
+constexpr int kNormParts = 1024;
 int orth_norm_parts() { return kNormParts; }
 
 hipError_t launch_orth_norm(ElemType t, const OrthInput &p, double *partial, hipStream_t stream)

@@ -185,6 +185,23 @@ def test_product_exact_with_one_scale_per_row(M, N, K):
     np.testing.assert_array_equal(cb, f32_to_bf16_rne(cf))
 
 
+@pytest.mark.parametrize("M,N,K", [(4352, 4352, 96), (4300, 14300, 64), (1200, 6000, 288), (4096, 4096, 160)])
+def test_product_of_many_tiles_exact(M, N, K):
+    """256-tiles in one launch and split by rows or columns into two, edges
+    included, every entry, against fp64 on the GPU (exact: one scale a row)."""
+    a, sa = mx_random(13, M, K, 0)
+    b, sb = mx_random(14, N, K, 0)
+    sa += (np.arange(M) % 5).astype(np.uint8)[:, None]
+    sb -= (np.arange(N) % 7).astype(np.uint8)[:, None]
+    want = (dev(ref.values(a, sa)) @ dev(ref.values(b, sb)).t())
+    args = (dev(ref.pack_codes(a)), dev(ref.pack_codes(b)), hkg.mx_pack_scales(dev(sa), A), hkg.mx_pack_scales(dev(sb), B))
+    Cf = torch.full((M, N), float("nan"), dtype=torch.float32, device="cuda")
+    C = hkg.gemm_mxfp4(*args, C_f32=Cf)
+    assert torch.equal(Cf.double(), want)
+    assert torch.equal(C, Cf.to(torch.bfloat16))
+    assert torch.equal(hkg.gemm_mxfp4(*args), C)
+
+
 def test_product_scale_nan_reaches_its_row_only():
     # also in the step that holds K's end, where the scales past it are read but not used
     for K in (96, 160, 256, 288):
