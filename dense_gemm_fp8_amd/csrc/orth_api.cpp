@@ -69,7 +69,7 @@ int pick_tile(int64_t M, int64_t N, bool triangle)
     return best;
 }
 
-// X <- a X + P X (m x n), whole or in the two parts of split_last_round.
+// X <- P X (m x n), whole or in the two parts of split_last_round.
 hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpilogue &e, hipStream_t stream)
 {
     const TileSplit split = tile == 256 ? split_last_round(p.M, p.N) : TileSplit{0, false};
@@ -83,7 +83,6 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
         head.M = keep;
         rest.M -= keep;
         rest.A = static_cast<const char *>(p.A) + skip;
-        re.D += keep * e.ldd;
         re.straight += e.straight ? keep * e.lds : 0;
         re.transposed += e.transposed ? keep : 0;
         re.cols_t -= keep;
@@ -91,10 +90,8 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
         head.N = keep;
         rest.N -= keep;
         rest.B = static_cast<const char *>(p.B) + skip;
-        re.D += keep;
         re.straight += e.straight ? keep : 0;
         re.cols_s -= keep;
-        re.cols_d -= keep;
         re.transposed += e.transposed ? keep * e.ldt : 0;
     }
     const hipError_t err = hkg::launch_orth_product(256, order_of(head.M, head.N, 2 * p.K, 256), false, head, e, stream);
@@ -176,23 +173,22 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
     rc = launched(tall ? hkg::launch_orth_convert(t, in, sums, eps, xt[0], mp, x, np, nullptr, 0, st)
                        : hkg::launch_orth_convert(t, in, sums, eps, x, np, xt[0], mp, nullptr, 0, st));
 
-    const float s = 1.0f / hkg::kOrthScale;   // a product of two scaled operands carries it twice
+    const float s = 1.0f / hkg::kOrthScale;
     const int sym = pick_tile(m, m, true), upd = pick_tile(m, n, false);
     for (int i = 0; i < steps && rc == HKG_OK; ++i) {
         const bool last = i + 1 == steps;
-        const _Float16 *x16 = reinterpret_cast<const _Float16 *>(x);
         // A = X X^T
         rc = launched(hkg::launch_orth_product(sym, order_of(m, m, 2 * np, sym), true, {x, x, m, m, np},
-                                               {s, 0.0f, nullptr, 0, 0, am, mp, mp, am, mp, mp, 0}, st));
-        // P = b A + c A A
+                                               {s * s, 0.0f, 0.0f, nullptr, 0, 0, am, mp, mp, am, mp, mp, 0}, st));
+        // P = a I + b A + c A A
         if (rc == HKG_OK)
             rc = launched(hkg::launch_orth_product(
                 sym, order_of(m, m, 2 * mp, sym), true, {am, am, m, m, mp},
-                {c * s, b, reinterpret_cast<const _Float16 *>(am), mp, mp, pm, mp, mp, pm, mp, mp, 0}, st));
-        // X <- a X + P X, as X and X^T, or the result in its own orientation
-        hkg::OrthEpilogue ep = {s, a, x16, np, np, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
+                {c, b, a, reinterpret_cast<const _Float16 *>(am), mp, mp, pm, mp, mp, pm, mp, mp, 0}, st));
+        // X <- P X, as X and X^T, or the result in its own orientation
+        hkg::OrthEpilogue ep = {1.0f, 0.0f, 0.0f, nullptr, 0, 0, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
         if (last) {
-            ep = {s * s, a * s, x16, np, np, nullptr, 0, 0, nullptr, 0, 0, 1};
+            ep = {s, 0.0f, 0.0f, nullptr, 0, 0, nullptr, 0, 0, nullptr, 0, 0, 1};
             if (tall) {
                 ep.transposed = static_cast<uint16_t *>(out);
                 ep.ldt = ldo;

@@ -10,7 +10,7 @@
 
 namespace hkg {
 
-// X, X X^T and b A + c A A are held as fp16 times this.
+// X is held as fp16 times this (the step's two symmetric matrices as they are).
 constexpr int kOrthScaleLog2 = 12;
 constexpr float kOrthScale = 1 << kOrthScaleLog2;
 
@@ -26,10 +26,10 @@ struct OrthProduct {
     int M, N, K;
 };
 
-// v = alpha (A B^T) + beta D, to straight [M] and / or transposed [N] (either null).
-// With a triangle of tiles both are the same symmetric matrix.
+// v = alpha (A B^T) + beta D + diag I, to straight [M] and / or transposed [N] (either
+// null).  With a triangle of tiles both are the same symmetric matrix.
 struct OrthEpilogue {
-    float alpha, beta;
+    float alpha, beta, diag;
     const _Float16 *D;   // [M], rows ldd elements apart, cols_d of each read, or null
     int64_t ldd;
     int cols_d;

@@ -126,11 +126,11 @@ int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, i
  *   out  [rows][cols] bf16, rows ldo elements apart (0 = cols); may be G itself
  *        when both are bf16 with one pitch, else must not overlap it
  *   steps 0 .. 64; eps >= 0 (a zero matrix stays zero)
- * X, A and b A + c A A are kept in fp16 between products (11-bit significands,
- * scaled by a power of two), sums are fp32; the polynomial must keep the
- * singular values of X below 2 and those of b A + c A A below 16 (beyond that
- * fp16 overflows to infinity), as the usual coefficients (3.4445, -4.7750,
- * 2.0315) do.  A NaN or an infinity in G makes every element of out NaN.
+ * X, A and a I + b A + c A A are kept in fp16 between products (11-bit
+ * significands; X scaled by a power of two), sums are fp32; the polynomial must
+ * keep the singular values of X below 15 (beyond that fp16 overflows to
+ * infinity), as the usual coefficients (3.4445, -4.7750, 2.0315) do.  A NaN or an
+ * infinity in G makes every element of out NaN.
  */
 int64_t hkg_orthogonalize_workspace_bytes(int64_t rows, int64_t cols);
 int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type, int64_t ldg,
