@@ -47,6 +47,11 @@ bool sizes_fit(int64_t rows, int64_t cols)
     return rows <= kMax && cols <= kMax;
 }
 
+// Up to so many 32 x 32 blocks a product runs on the kernel for small matrices (five
+// steps on it against five on tiles: 256 x 256 68 us against 108, 1024 x 2048 -- 2048
+// blocks in its third product -- 213 against 236, 2048 x 2048 665 against 336).
+constexpr int64_t kSmallBlocks = 2048;
+
 // The tile of a product (M x N, or the triangle of an M x M): the one whose rounds
 // of the 256 compute units take least, a unit's time for a tile growing with its
 // area and, for smaller tiles, with the LDS bytes per matrix instruction (two
@@ -54,6 +59,9 @@ bool sizes_fit(int64_t rows, int64_t cols)
 // split off (split_last_round), where that is done.
 int pick_tile(int64_t M, int64_t N, bool triangle)
 {
+    const int64_t bm = pad64(M) / 32, bn = pad64(N) / 32;
+    if ((triangle ? bm * (bm + 1) / 2 : bm * bn) <= kSmallBlocks)
+        return 32;
     int best = 256;
     double least = 0.0;
     for (const int t : {256, 192, 128}) {
@@ -69,12 +77,19 @@ int pick_tile(int64_t M, int64_t N, bool triangle)
     return best;
 }
 
+// Tiles cover the padding of a result's rows and columns too (multiples of 64): it
+// holds zeros where the next product takes it for K.
+hkg::TileOrder tiles_of(int64_t M, int64_t N, int64_t K, int tile)
+{
+    return order_of(pad64(M), pad64(N), 2 * K, tile);
+}
+
 // X <- P X (m x n), whole or in the two parts of split_last_round.
 hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpilogue &e, hipStream_t stream)
 {
     const TileSplit split = tile == 256 ? split_last_round(p.M, p.N) : TileSplit{0, false};
     if (split.keep == 0)
-        return hkg::launch_orth_product(tile, order_of(p.M, p.N, 2 * p.K, tile), false, p, e, stream);
+        return hkg::launch_orth_product(tile, tiles_of(p.M, p.N, p.K, tile), false, p, e, stream);
     hkg::OrthProduct head = p, rest = p;
     hkg::OrthEpilogue re = e;
     const int keep = static_cast<int>(split.keep);
@@ -94,10 +109,10 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
         re.cols_s -= keep;
         re.transposed += e.transposed ? keep * e.ldt : 0;
     }
-    const hipError_t err = hkg::launch_orth_product(256, order_of(head.M, head.N, 2 * p.K, 256), false, head, e, stream);
+    const hipError_t err = hkg::launch_orth_product(256, tiles_of(head.M, head.N, p.K, 256), false, head, e, stream);
     if (err != hipSuccess)
         return err;
-    return hkg::launch_orth_product(128, order_of(rest.M, rest.N, 2 * p.K, 128), false, rest, re, stream);
+    return hkg::launch_orth_product(128, tiles_of(rest.M, rest.N, p.K, 128), false, rest, re, stream);
 }
 
 }  // namespace
@@ -178,12 +193,12 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
     for (int i = 0; i < steps && rc == HKG_OK; ++i) {
         const bool last = i + 1 == steps;
         // A = X X^T
-        rc = launched(hkg::launch_orth_product(sym, order_of(m, m, 2 * np, sym), true, {x, x, m, m, np},
+        rc = launched(hkg::launch_orth_product(sym, tiles_of(m, m, np, sym), true, {x, x, m, m, np},
                                                {s * s, 0.0f, 0.0f, nullptr, 0, 0, am, mp, mp, am, mp, mp, 0}, st));
         // P = a I + b A + c A A
         if (rc == HKG_OK)
             rc = launched(hkg::launch_orth_product(
-                sym, order_of(m, m, 2 * mp, sym), true, {am, am, m, m, mp},
+                sym, tiles_of(m, m, mp, sym), true, {am, am, m, m, mp},
                 {c, b, a, reinterpret_cast<const _Float16 *>(am), mp, mp, pm, mp, mp, pm, mp, mp, 0}, st));
         // X <- P X, as X and X^T, or the result in its own orientation
         hkg::OrthEpilogue ep = {1.0f, 0.0f, 0.0f, nullptr, 0, 0, x, np, np, xt[(i + 1) & 1], mp, mp, 0};

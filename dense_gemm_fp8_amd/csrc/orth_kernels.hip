@@ -277,6 +277,125 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
     }
 }
 
+// ---- a product of a step on a small matrix -----------------------------------
+// What bounds it is the way to memory and back, once a launch and 15 launches an
+// update: a workgroup takes 32 x 32 results and its 8 waves split K, each sending all
+// loads of a 64-k run at once (whole lines, into LDS of its own) and multiplying when
+// they are there; their sums are joined in LDS in a fixed order.  256 x 256: 4 us a
+// product, launch included, against 6.5 on 128-tiles, whose loop keeps two K steps in
+// flight.
+constexpr int kSmallWaves = 8;
+constexpr int kSmallPanel = 32 * kStepBytes;   // 32 rows of a run
+
+template <bool kBf16>
+__global__ __launch_bounds__(64 * kSmallWaves) void orth_small_kernel(const TileOperands o, const OrthEpilogue p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[kSmallWaves * 2 * kSmallPanel];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int tm, tn;
+    if (o.triangle) {
+        triangle_tile(blockIdx.x, o.Gm, tm, tn);
+    } else {
+        tm = blockIdx.x / o.Gn;
+        tn = blockIdx.x % o.Gn;
+    }
+    const int row0 = 32 * tm, col0 = 32 * tn, rows = min(32, o.rows_a - row0), cols = min(32, o.rows_b - col0);
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(static_cast<const char *>(o.A) + (int64_t)row0 * o.pitch_a,
+                                                panel_range(rows, o.pitch_a, o.kb));
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(static_cast<const char *>(o.B) + (int64_t)col0 * o.pitch_b,
+                                                panel_range(cols, o.pitch_b, o.kb));
+    char *const la = smem + wave * 2 * kSmallPanel, *const lb = la + kSmallPanel;
+    auto send = [&](int t) {
+#pragma unroll
+        for (int d = 0; d < kSmallPanel / kLoadBytes; ++d) {
+            const int row = 8 * d + (lane >> 3), at = t * kStepBytes + (((lane & 7) ^ swz_a(row)) << 4);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void *)(la + d * kLoadBytes), 16,
+                                                     row * o.pitch_a + at, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (__attribute__((address_space(3))) void *)(lb + d * kLoadBytes), 16,
+                                                     row * o.pitch_b + at, 0, 0, 0);
+        }
+    };
+    const int x = lane & 15, q = lane >> 4;
+    f32x4_t acc[2][2] = {};
+    if (wave < o.nk)
+        send(wave);
+    for (int t = wave; t < o.nk; t += kSmallWaves) {
+        wait_loads<0>();
+        f16x8_t a[2][2], b[2][2];   // [slice][block]
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = (16 * i + x) * kStepBytes + (((4 * s + q) ^ swz_a(16 * i + x)) << 4);
+                a[s][i] = *reinterpret_cast<const f16x8_t *>(la + at);
+                b[s][i] = *reinterpret_cast<const f16x8_t *>(lb + at);
+            }
+        wait_lds();   // the fragments are in registers: their LDS is free
+        if (t + kSmallWaves < o.nk)
+            send(t + kSmallWaves);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[s][j], a[s][i], acc[i][j], 0, 0, 0);
+    }
+    settle(acc);
+    __syncthreads();
+    // [wave][row][column], rows 33 apart: lane (x, q) of block (i, j) holds row 16 i + x,
+    // columns 16 j + 4 q ..
+    float(*part)[32][33] = reinterpret_cast<float(*)[32][33]>(smem);
+    static_assert(kSmallWaves * 32 * 33 * 4 <= kSmallWaves * 2 * kSmallPanel, "the sums fit");
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wave][16 * i + x][16 * j + 4 * q + e] = acc[i][j][e];
+    __syncthreads();
+    // a thread takes two neighbouring columns of a row, then two neighbouring rows of a
+    // column (the same results, summed again in the same order)
+#pragma unroll
+    for (int way = 0; way < 2; ++way) {
+        uint16_t *const to = way == 0 ? p.straight : p.transposed;
+        if (!to)
+            continue;
+        const int fast = 2 * (threadIdx.x & 15), slow = threadIdx.x >> 4;
+        uint16_t w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = way == 0 ? slow : fast + e, c = way == 0 ? fast + e : slow;
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSmallWaves; ++k)
+                s += part[k][r][c];
+            float v = p.alpha * s;
+            if (p.D) {
+                if (r < rows && col0 + c < p.cols_d)
+                    v += p.beta * (float)p.D[(row0 + r) * p.ldd + col0 + c];
+                v += row0 + r == col0 + c ? p.diag : 0.0f;
+            }
+            w[e] = kBf16 ? (uint16_t)pack2_bf16(v, 0.f) : __builtin_bit_cast(uint16_t, (_Float16)v);
+        }
+        const int64_t ld = way == 0 ? p.lds : p.ldt;
+        const int line = (way == 0 ? row0 : col0) + slow, at = (way == 0 ? col0 : row0) + fast;
+        const int lines = way == 0 ? o.rows_a : o.rows_b, width = way == 0 ? p.cols_s : p.cols_t;
+        if (line >= lines)
+            continue;
+        uint16_t *const d = to + line * ld + at;
+        if (at + 1 < width && (reinterpret_cast<uintptr_t>(d) & 3) == 0) {
+            *reinterpret_cast<uint32_t *>(d) = w[0] | (uint32_t)w[1] << 16;
+        } else {
+            if (at < width)
+                d[0] = w[0];
+            if (at + 1 < width)
+                d[1] = w[1];
+        }
+    }
+}
+
 }  // namespace
 
 constexpr int kNormParts = 1024;
@@ -313,6 +432,8 @@ static hipError_t launch_product(int tile, const TileOperands &o, const OrthEpil
         hipLaunchKernelGGL((orth_product_kernel<256, kBf16>), grid, block, 0, stream, o, e);
     else if (tile == 192)
         hipLaunchKernelGGL((orth_product_kernel<192, kBf16>), grid, block, 0, stream, o, e);
+    else if (tile == 32)
+        hipLaunchKernelGGL(orth_small_kernel<kBf16>, grid, dim3(64 * kSmallWaves), 0, stream, o, e);
     else
         hipLaunchKernelGGL((orth_product_kernel<128, kBf16>), grid, block, 0, stream, o, e);
     return hipGetLastError();
