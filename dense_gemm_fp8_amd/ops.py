@@ -88,9 +88,9 @@ def _pad32(k: int) -> int:
     return (k + 31) & ~31
 
 
-def _scale_bytes(rows: int, kp: int) -> int:
-    """hkg_mx_packed_scale_bytes for sizes the call itself will check."""
-    return ((rows + 127) >> 7) * ((kp + 127) >> 7) * 512
+def _scale_bytes(rows: int, k: int) -> int:
+    """hkg_mx_packed_scale_bytes(rows, k padded) for sizes the call itself will check."""
+    return ((rows + 127) >> 7) * ((k + 127) >> 7) * 512
 
 
 def _elem_type(t, name) -> int:
@@ -108,17 +108,21 @@ def _codes(t, rows, K, name):
     import torch
     if t.dtype is not torch.uint8 or t.dim() != 2:
         raise TypeError("%s must be a 2-D uint8 tensor of e2m1 codes" % name)
-    if tuple(t.shape) != (rows, _pad32(K) >> 1):
+    if t.shape != (rows, _pad32(K) >> 1):
         raise ValueError("%s must be [%d, %d]" % (name, rows, _pad32(K) >> 1))
-    return _hkg._dev_ptr(t, name)
+    return _dense(t, name)
 
 
 def _packed(t, rows, K, name):
     import torch
-    need = _scale_bytes(rows, _pad32(K))
+    need = _scale_bytes(rows, K)
     if t.dtype is not torch.uint8 or t.numel() < need:
         raise ValueError("%s must be a uint8 tensor of at least %d bytes" % (name, need))
-    return _hkg._dev_ptr(t, name)
+    return _dense(t, name)
+
+
+def _dense(t, name):
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _hkg._dev_ptr(t, name)
 
 
 def _handle(stream, t) -> int:
@@ -147,7 +151,7 @@ def _output(t, shape, dtype, name, like, stream):
     if t is None:
         t = _empty(shape, dtype, like, stream)
         return t, t.data_ptr(), shape[1]
-    if tuple(t.shape) != shape or t.dtype is not dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s must be a %s tensor of shape %s" % (name, dtype, shape))
     ptr, ld = _hkg._matrix(t, name)
     return t, ptr, ld
