@@ -10,12 +10,11 @@ namespace hkg {
 namespace {
 
 template <int kT>
-__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const TileOperands o, const Mx4GemmParams p)
+__device__ __forceinline__ void mx4_tile(const TileOperands &o, const Mx4GemmParams &p, int block, char *smem)
 {
     using Loop = TileLoop<F4, kT>;
-    __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
     int tm, tn;
-    remap_tile(blockIdx.x, o.Gm, o.Gn, o.W, o.C, tm, tn);
+    remap_tile(block, o.Gm, o.Gn, o.W, o.C, tm, tn);
     f32x4_t acc[Loop::kB][Loop::kB];
 #pragma unroll
     for (int i = 0; i < Loop::kB; ++i)
@@ -58,9 +57,33 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const 
             }
 }
 
+template <int kT>
+__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const TileOperands o, const Mx4GemmParams p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[TileLoop<F4, kT>::kLds];
+    mx4_tile<kT>(o, p, blockIdx.x, smem);
+}
+
+// Two products: the first `first` workgroups (a multiple of 8: both orders count on
+// workgroup b running on XCD b mod 8) are product 0's tiles, padded, the rest product 1's.
+struct TilePair {
+    TileOperands o[2];
+    Mx4GemmParams p[2];
+    int first;
+};
+template <int kT>
+__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_pair_kernel(const TilePair t)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[TileLoop<F4, kT>::kLds];
+    const int which = (int)blockIdx.x >= t.first, block = blockIdx.x - (which ? t.first : 0);
+    const TileOperands o = t.o[which];
+    if (block < o.Gm * o.Gn)
+        mx4_tile<kT>(o, t.p[which], block, smem);
+}
+
 }  // namespace
 
-hipError_t launch_mx4_tiles(int tile, const TileOrder &order, const Mx4GemmParams &p, hipStream_t stream)
+static TileOperands operands(const TileOrder &order, const Mx4GemmParams &p)
 {
     TileOperands o = {};
     o.A = p.A;
@@ -78,6 +101,26 @@ hipError_t launch_mx4_tiles(int tile, const TileOrder &order, const Mx4GemmParam
     const int64_t steps = (p.kb + 63) / 64;
     o.sa_bytes = (int)((p.M + 127) / 128 * steps * kMxStepScales);
     o.sb_bytes = (int)((p.N + 127) / 128 * steps * kMxStepScales);
+    return o;
+}
+
+hipError_t launch_mx4_tiles2(int tile, const TileOrder &order, const Mx4GemmParams &p, const TileOrder &order2,
+                             const Mx4GemmParams &p2, hipStream_t stream)
+{
+    TilePair t = {{operands(order, p), operands(order2, p2)}, {p, p2}, (order.Gm * order.Gn + 7) / 8 * 8};
+    const dim3 grid((unsigned)t.first + (unsigned)order2.Gm * (unsigned)order2.Gn), block(256);
+    if (tile == 256)
+        hipLaunchKernelGGL(mx4_tile_pair_kernel<256>, grid, block, 0, stream, t);
+    else if (tile == 128)
+        hipLaunchKernelGGL(mx4_tile_pair_kernel<128>, grid, block, 0, stream, t);
+    else
+        return hipErrorInvalidValue;
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_tiles(int tile, const TileOrder &order, const Mx4GemmParams &p, hipStream_t stream)
+{
+    const TileOperands o = operands(order, p);
     const dim3 grid((unsigned)order.Gm * (unsigned)order.Gn), block(256);
     if (tile == 256)
         hipLaunchKernelGGL(mx4_tile_kernel<256>, grid, block, 0, stream, o, p);

@@ -214,14 +214,13 @@ struct FewRows {
 };
 
 template <int kXt, int kMb, int kS>
-__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(const Mx4GemmParams p)
+__device__ __forceinline__ void mx4_few_rows(const Mx4GemmParams &p, int block, char *smem)
 {
     using G = FewRows<kXt, kMb, kS>;
-    __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, q = lane >> 4;
     const int gn = (p.N + 31) / 32;
-    const int n0 = 32 * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
+    const int n0 = 32 * (block % gn), m0 = 16 * kMb * (block / gn);
     const int nk = (p.kb + 63) / 64;              // 128-k steps
     const int g = n0 >> 7, j = (n0 >> 5) & 3;     // B's packed group, pair of fragments in it
     const uint32_t span = (uint32_t)nk * kMxStepScales;
@@ -389,6 +388,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(const Mx4G
     }
 }
 
+template <int kXt, int kMb, int kS>
+__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(const Mx4GemmParams p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[FewRows<kXt, kMb, kS>::kLds];
+    mx4_few_rows<kXt, kMb, kS>(p, blockIdx.x, smem);
+}
+
+// Two products: the first `first` workgroups are product 0's.
+struct FewRowsPair {
+    Mx4GemmParams p[2];
+    int first;
+};
+template <int kMb, int kS>
+__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_pair_kernel(const FewRowsPair t)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[FewRows<-1, kMb, kS>::kLds];
+    const int which = (int)blockIdx.x >= t.first;
+    mx4_few_rows<-1, kMb, kS>(t.p[which], blockIdx.x - (which ? t.first : 0), smem);
+}
+
 }  // namespace
 
 hipError_t launch_mx4_quantize(ElemType t, const QuantParams &p, hipStream_t stream)
@@ -425,14 +444,21 @@ static hipError_t few_rows(const Mx4GemmParams &p, unsigned blocks, hipStream_t 
     return hipGetLastError();
 }
 
+// Two-step runs (96 KiB of LDS at 64 rows) where each of 256 compute units has at most
+// one workgroup, or for a long K: 256 x 4096 x 14336 24.4 us against 27.1 in one-step
+// runs, which let three workgroups share a unit (256 x 4096 x 4096: 9.3 against 10.5).
+static bool two_steps(unsigned blocks, int K) { return blocks <= 256 || K >= 8192; }
+
+static unsigned few_blocks(const Mx4GemmParams &p, int mb)
+{
+    return (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
+}
+
 hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream)
 {
     const int mb = p.A && p.M > 16 ? 4 : 1;
-    const unsigned blocks = (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
-    // two-step runs (96 KiB of LDS) where each of 256 compute units has at most one
-    // workgroup, or for a long K: 256 x 4096 x 14336 24.4 us against 27.1 in one-step
-    // runs, which let three workgroups share a unit (256 x 4096 x 4096: 9.3 against 10.5)
-    const bool two = blocks <= 256 || p.K >= 8192;
+    const unsigned blocks = few_blocks(p, mb);
+    const bool two = two_steps(blocks, p.K);
     if (p.A) {
         if (mb == 1)   // 48 KiB in two-step runs
             return few_rows<-1, 1, 2>(p, blocks, stream);
@@ -441,6 +467,17 @@ hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t 
     if (xt == kElemF32)   // 80 KiB in one-step runs
         return few_rows<1, 1, 1>(p, blocks, stream);
     return two ? few_rows<0, 1, 2>(p, blocks, stream) : few_rows<0, 1, 1>(p, blocks, stream);
+}
+
+hipError_t launch_mx4_few_rows2(const Mx4GemmParams &p, const Mx4GemmParams &p2, hipStream_t stream)
+{
+    const unsigned first = few_blocks(p, 4), blocks = first + few_blocks(p2, 4);
+    const FewRowsPair t = {{p, p2}, (int)first};
+    if (two_steps(blocks, p.K > p2.K ? p.K : p2.K))
+        hipLaunchKernelGGL((mx4_few_rows_pair_kernel<4, 2>), dim3(blocks), dim3(64 * kFewWaves), 0, stream, t);
+    else
+        hipLaunchKernelGGL((mx4_few_rows_pair_kernel<4, 1>), dim3(blocks), dim3(64 * kFewWaves), 0, stream, t);
+    return hipGetLastError();
 }
 
 }  // namespace hkg

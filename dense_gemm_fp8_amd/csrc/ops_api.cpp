@@ -96,12 +96,20 @@ hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const
 // 9.3 us against 10.7 on 128-tiles, 512 x 2048 x 2048 6.3 against 7.2, 256 x 4096 x 14336
 // 24.4 against 35.8; at 896 and 1024: 128 x 14336 x 4096 17.6 against 13.4, 256 x 8192 x
 // 8192 34.5 against 23.2.
+int product_tile(const hkg::Mx4GemmParams &p)   // 0: the kernel for few rows
+{
+    if (ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
+        return 0;
+    return ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128 ? 128 : 256;
+}
+
 hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 {
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
+    const int tile = product_tile(p);
+    if (tile == 0)
         return hkg::launch_mx4_few_rows(hkg::kElemBf16, p, st);
-    if (ceil_div(p.M, 256) * ceil_div(p.N, 256) <= 128)
+    if (tile == 128)
         return hkg::launch_mx4_tiles(128, order_of(p.M, p.N, p.kb, 128), p, st);
     const TileSplit split = split_last_round(p.M, p.N);
     hkg::Mx4GemmParams head = p, rest = p;
@@ -120,6 +128,24 @@ hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
     if (e != hipSuccess || split.keep == 0)
         return e;
     return hkg::launch_mx4_tiles(128, order_of(rest.M, rest.N, p.kb, 128), rest, st);
+}
+
+// Two independent products, in one launch where both take the same kernel: a launch less
+// for small ones (the gradients of 500 x 1000 x 768: 17.2 us against 20.8), one partial
+// last round instead of two for large ones, the longer tiles first (8192 x 14336 x 4096:
+// 484 us against 490).
+hipError_t run_products(const hkg::Mx4GemmParams &p, const hkg::Mx4GemmParams &p2, void *stream)
+{
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int tile = product_tile(p);
+    if (tile != product_tile(p2)) {
+        const hipError_t e = run_product(p, stream);
+        return e != hipSuccess ? e : run_product(p2, stream);
+    }
+    if (tile == 0)
+        return hkg::launch_mx4_few_rows2(p, p2, st);
+    const hkg::Mx4GemmParams &a = p.kb >= p2.kb ? p : p2, &b = p.kb >= p2.kb ? p2 : p;
+    return hkg::launch_mx4_tiles2(tile, order_of(a.M, a.N, a.kb, tile), a, order_of(b.M, b.N, b.kb, tile), b, st);
 }
 
 // Whether the linear layer quantises x inside the product: up to 16 rows, whose part of
@@ -339,11 +365,11 @@ int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, i
                                     HKG_MX_OPERAND_A, q, s, want_w ? qt : nullptr, want_w ? stt : nullptr};
         rc = launched(hkg::launch_mx4_quantize(dy_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16, p, st));
     }
-    if (rc == HKG_OK && want_x)
-        rc = launched(run_product(product(M, K, N, q, s, Wt, SWt, dx, nullptr, lddx), stream));
-    if (rc == HKG_OK && want_w)
-        rc = launched(run_product(product(N, K, M, qt, stt, Xt, SXt, dw, nullptr, lddw), stream));
-    return rc;
+    if (rc != HKG_OK)
+        return rc;
+    const hkg::Mx4GemmParams px = product(M, K, N, q, s, Wt, SWt, dx, nullptr, lddx);
+    const hkg::Mx4GemmParams pw = product(N, K, M, qt, stt, Xt, SXt, dw, nullptr, lddw);
+    return launched(want_x && want_w ? run_products(px, pw, stream) : run_product(want_x ? px : pw, stream));
 }
 
 }  // extern "C"

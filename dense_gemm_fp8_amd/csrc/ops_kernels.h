@@ -43,6 +43,8 @@ struct Mx4GemmParams {
     int M, N, K, kb;
 };
 hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
+// Two products in one launch (both A's are codes).
+hipError_t launch_mx4_few_rows2(const Mx4GemmParams &p, const Mx4GemmParams &p2, hipStream_t stream);
 
 // A grid of Gm x Gn tiles and the order its workgroups walk it in (remap.h).
 struct TileOrder {
@@ -50,5 +52,8 @@ struct TileOrder {
 };
 // The same product on tile x tile output tiles (256 or 128); A is codes.
 hipError_t launch_mx4_tiles(int tile, const TileOrder &order, const Mx4GemmParams &p, hipStream_t stream);
+// Two products in one launch, the first one's tiles first.
+hipError_t launch_mx4_tiles2(int tile, const TileOrder &order, const Mx4GemmParams &p, const TileOrder &order2,
+                             const Mx4GemmParams &p2, hipStream_t stream);
 
 }  // namespace hkg

@@ -510,26 +510,27 @@ struct Stage {
 
 // Stores a staged quarter (rows x cols of it exist, at `to`, rows ld elements apart):
 // 16 lanes (8 or 12 of them for smaller tiles) write one row.  units: rows start
-// 16-byte aligned and cols is whole units, else element by element.
+// 16-byte aligned and cols is whole units; else neighbouring lanes write neighbouring
+// elements (1111 x 2777 x 1184 e2m1: 8.8 us, against 12.2 with a unit's elements
+// stored one after the other by one lane).
 template <int kB>
 __device__ __forceinline__ void store_stage(const Stage<kB> &st, int lane, uint16_t *to, int64_t ld, int rows, int cols,
                                             bool units)
 {
     constexpr int kUnits = Stage<kB>::kUnits, kSide = Stage<kB>::kSide;
     rows = min(rows, kSide);
-    const __amdgpu_buffer_rsrc_t rs = buffer_of(to, units && rows > 0 ? (uint32_t)rows * (uint32_t)(2 * ld) : 0u);
+    if (!units) {
+        for (int row = 0; row < rows; ++row)
+            for (int c = lane; c < min(cols, kSide); c += 64)
+                to[row * ld + c] = st.base[Stage<kB>::place(row, c >> 3) + (c & 7)];
+        return;
+    }
+    const __amdgpu_buffer_rsrc_t rs = buffer_of(to, rows > 0 ? (uint32_t)rows * (uint32_t)(2 * ld) : 0u);
 #pragma unroll 8
     for (int k = 0; k < kSide * kUnits / 64; ++k) {
         const int at = 64 * k + lane, row = at / kUnits, u = at % kUnits;
-        const u32x4_t w = *st.unit(row, u);
-        if (units) {
-            __builtin_amdgcn_raw_buffer_store_b128(w, rs, 8 * u < cols ? (int)(2 * (row * ld + 8 * u)) : kPastEnd, 0, 0);
-        } else if (row < rows) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * u + e < cols)
-                    to[row * ld + 8 * u + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        }
+        __builtin_amdgcn_raw_buffer_store_b128(*st.unit(row, u), rs,
+                                               8 * u < cols ? (int)(2 * (row * ld + 8 * u)) : kPastEnd, 0, 0);
     }
 }
 
