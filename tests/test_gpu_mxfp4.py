@@ -159,7 +159,7 @@ def check_product(cb, cf, want, tol, what):
 
 
 SHAPES = [(1, 1, 32), (1, 40, 64), (16, 32, 128), (17, 33, 160), (100, 300, 96), (128, 128, 256), (129, 257, 416),
-          (256, 256, 512), (300, 520, 1056), (513, 260, 224), (640, 1100, 2048)]
+          (256, 256, 512), (300, 520, 1056), (513, 260, 224), (640, 1100, 2048), (500, 1100, 352)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -202,14 +202,39 @@ def test_product_of_many_tiles_exact(M, N, K):
     assert torch.equal(hkg.gemm_mxfp4(*args), C)
 
 
-def test_product_scale_nan_reaches_its_row_only():
+def gpu_bound(va, vb, K):
+    """|C_f32 - exact| from the summation bound, with a row's largest values in the
+    place of a step's."""
+    top = va.abs().amax(1)[:, None] * vb.abs().amax(1)[None, :]
+    total = va.abs() @ vb.abs().t()
+    return (K // 128 + 1) * (2.0 ** -6 * top + 2.0 ** -24 * total)
+
+
+@pytest.mark.parametrize("M,N,K", [(1500, 1300, 544), (1100, 2777, 1184), (4352, 4352, 416), (4096, 8192, 288)])
+def test_product_of_many_tiles_with_block_scales(M, N, K):
+    """128- and 256-tiles with scales of their own in every block, every entry,
+    against fp64 on the GPU."""
+    a, sa = mx_random(15, M, K, 1)
+    b, sb = mx_random(16, N, K, 1)
+    va, vb = dev(ref.values(a, sa)), dev(ref.values(b, sb))
+    Cf = torch.full((M, N), float("nan"), dtype=torch.float32, device="cuda")
+    C = hkg.gemm_mxfp4(dev(ref.pack_codes(a)), dev(ref.pack_codes(b)), hkg.mx_pack_scales(dev(sa), A),
+                       hkg.mx_pack_scales(dev(sb), B), C_f32=Cf)
+    off = (Cf.double() - va @ vb.t()).abs()
+    assert bool((off <= gpu_bound(va, vb, K)).all()), "largest error %g" % off.max()
+    assert torch.equal(C, Cf.to(torch.bfloat16))
+
+
+# few rows, 128-tiles and 256-tiles
+@pytest.mark.parametrize("M,N", [(140, 150), (1500, 1300), (4200, 4000)])
+def test_product_scale_nan_reaches_its_row_only(M, N):
     # also in the step that holds K's end, where the scales past it are read but not used
     for K in (96, 160, 256, 288):
-        a, sa = mx_random(5, 140, K, 2)
-        b, sb = mx_random(6, 150, K, 2)
+        a, sa = mx_random(5, M, K, 2)
+        b, sb = mx_random(6, N, K, 2)
         sa[7, -1] = sb[139, 0] = 255
         cb, cf = run_product(a, sa, b, sb)
-        bad = np.zeros((140, 150), dtype=bool)
+        bad = np.zeros((M, N), dtype=bool)
         bad[7] = bad[:, 139] = True
         assert np.isnan(cf[bad]).all() and np.isfinite(cf[~bad]).all()
 
@@ -241,7 +266,8 @@ def test_empty_products():
 
 
 LINEAR = [(1, 1, 1), (1, 64, 33), (1, 1000, 4096), (2, 130, 100), (7, 257, 520), (16, 512, 1000), (17, 64, 96),
-          (31, 300, 700), (100, 200, 257), (128, 384, 512), (257, 129, 640)]
+          (31, 300, 700), (100, 200, 257), (128, 384, 512), (257, 129, 640), (5, 8300, 160), (16, 8300, 97),
+          (3, 70, 10272), (16, 40, 12000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -299,6 +325,23 @@ def test_backward_against_the_formula(M, N, K, dtype):
         got = host(got.float())
         bad = ~(np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol))
         assert not bad.any(), "%s: %d off" % (what, bad.sum())
+
+
+@pytest.mark.parametrize("M,N,K", [(1100, 1300, 1500), (300, 2500, 2600), (4200, 4352, 4400)])
+def test_backward_on_tiles(M, N, K):
+    """Gradients whose products run as 128- or 256-tiles, in one launch or (few rows
+    and tiles) in two, against fp64 on the GPU."""
+    dy = torch.randn(M, N, device="cuda", generator=torch.Generator("cuda").manual_seed(M)).to(torch.bfloat16)
+    q, s, qt, st = hkg.mxfp4_quantize_both(dy, A, A)          # checked bit for bit above
+    W, x = torch.randn(N, K, device="cuda"), torch.randn(M, K, device="cuda")
+    _, _, wt, swt = hkg.mxfp4_quantize_both(W, B, B)
+    _, _, xt, sxt = hkg.mxfp4_quantize_both(x, A, B)
+    dx, dw = hkg.linear_mxfp4_backward(dy, wt, swt, xt, sxt)
+    v = lambda c, p, o: hkg.mxfp4_dequantize(c, p, o, dtype=torch.float32).double()  # noqa: E731
+    for got, l, r, k in ((dx, v(q, s, A), v(wt, swt, B), N), (dw, v(qt, st, A), v(xt, sxt, B), M)):
+        want = l @ r.t()
+        tol = gpu_bound(l, r, k)
+        assert bool(((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
 
 
 def test_backward_against_differences():
