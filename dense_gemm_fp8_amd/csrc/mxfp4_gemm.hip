@@ -31,6 +31,8 @@ __device__ __forceinline__ void mx4_tile(const TileOperands &o, const Mx4GemmPar
     const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
     barrier();   // every wave has read its last fragments
     const Stage<kB> st(smem, loop.wave);
+    const int64_t at = row0 * p.ldc + col0;
+    const StageOut<kB> out(p.C, at, p.ldc, p.M - row0, p.N - col0, p.N);
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
         settle_row(acc, i);
@@ -40,9 +42,11 @@ __device__ __forceinline__ void mx4_tile(const TileOperands &o, const Mx4GemmPar
             *st.unit(16 * i + x, 4 * h + q) = u32x4_t{pack2_bf16(lo[0], lo[1]), pack2_bf16(lo[2], lo[3]),
                                                       pack2_bf16(hi[0], hi[1]), pack2_bf16(hi[2], hi[3])};
         }
+        if (i > 0)
+            out.rows16(st, loop.lane, 16 * (i - 1));   // while the next rows are converted
     }
-    const int64_t at = row0 * p.ldc + col0;
-    store_stage(st, loop.lane, p.C + at, p.ldc, p.M - row0, p.N - col0, ((p.N | p.ldc) & 7) == 0 && p.ldc < (1 << 22));
+    out.rows16(st, loop.lane, 16 * (kB - 1));
+    out.odd_rows(st, loop.lane);
     if (!p.C_f32)
         return;
 #pragma unroll

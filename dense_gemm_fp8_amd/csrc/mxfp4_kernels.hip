@@ -177,7 +177,7 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams
 // the waves' sums are joined in LDS at the end, in a fixed order.  The detour through
 // LDS is what makes the loads whole lines: a lane of a fragment holds 16 bytes of a row
 // of its own, and loaded straight into registers every lane is a request of its own
-// (16 x 8192 x 8192: 15.4 us so, x among them, against .. through LDS).
+// (16 x 8192 x 8192: 15.4 us so, x among them, against 11.4 through LDS).
 // B is the matrix instruction's first operand: fragments 2 j and 2 j + 1 of a packed
 // group then give a lane 8 consecutive columns of one row of C.  kXt: -1 A is codes, 0
 // / 1 x is bf16 / fp32 and each lane quantises the one block that its fragment holds (16

@@ -508,31 +508,48 @@ struct Stage {
     }
 };
 
-// Stores a staged quarter (rows x cols of it exist, at `to`, rows ld elements apart):
-// 16 lanes (8 or 12 of them for smaller tiles) write one row.  units: rows start
-// 16-byte aligned and cols is whole units; else neighbouring lanes write neighbouring
-// elements (1111 x 2777 x 1184 e2m1: 8.8 us, against 12.2 with a unit's elements
-// stored one after the other by one lane).
+// Where a staged quarter goes: `to`, rows ld elements apart, of which rows x cols exist.
+// Rows that start 16-byte aligned and hold whole units leave 16 at a time (rows16), as
+// soon as they are staged, 16 lanes (8 or 12 for smaller tiles) to a row; others at the
+// end (odd_rows), neighbouring lanes writing neighbouring elements (1111 x 2777 x 1184
+// e2m1: 8.8 us, against 12.2 with a unit's elements stored one after the other by one
+// lane).
 template <int kB>
-__device__ __forceinline__ void store_stage(const Stage<kB> &st, int lane, uint16_t *to, int64_t ld, int rows, int cols,
-                                            bool units)
-{
-    constexpr int kUnits = Stage<kB>::kUnits, kSide = Stage<kB>::kSide;
-    rows = min(rows, kSide);
-    if (!units) {
+struct StageOut {
+    using St = Stage<kB>;
+    uint16_t *to;
+    int64_t ld;
+    int rows, cols;
+    bool units;
+    __amdgpu_buffer_rsrc_t rs;
+
+    __device__ __forceinline__ StageOut(uint16_t *base, int64_t at, int64_t pitch, int r, int c, int width)
+        : to(base + at), ld(pitch), rows(min(r, St::kSide)), cols(c)
+    {
+        units = ((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(2 * pitch) | (uintptr_t)(2 * width)) & 15) == 0 &&
+                pitch < (1 << 22);
+        rs = buffer_of(to, units && rows > 0 ? (uint32_t)rows * (uint32_t)(2 * ld) : 0u);
+    }
+    __device__ __forceinline__ void rows16(const St &st, int lane, int r0) const
+    {
+        if (!units)
+            return;
+#pragma unroll
+        for (int k = 0; k < 16 * St::kUnits / 64; ++k) {
+            const int at = 64 * k + lane, row = r0 + at / St::kUnits, u = at % St::kUnits;
+            __builtin_amdgcn_raw_buffer_store_b128(*st.unit(row, u), rs,
+                                                   8 * u < cols ? (int)(2 * (row * ld + 8 * u)) : kPastEnd, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void odd_rows(const St &st, int lane) const
+    {
+        if (units)
+            return;
         for (int row = 0; row < rows; ++row)
-            for (int c = lane; c < min(cols, kSide); c += 64)
-                to[row * ld + c] = st.base[Stage<kB>::place(row, c >> 3) + (c & 7)];
-        return;
+            for (int c = lane; c < min(cols, St::kSide); c += 64)
+                to[row * ld + c] = st.base[St::place(row, c >> 3) + (c & 7)];
     }
-    const __amdgpu_buffer_rsrc_t rs = buffer_of(to, rows > 0 ? (uint32_t)rows * (uint32_t)(2 * ld) : 0u);
-#pragma unroll 8
-    for (int k = 0; k < kSide * kUnits / 64; ++k) {
-        const int at = 64 * k + lane, row = at / kUnits, u = at % kUnits;
-        __builtin_amdgcn_raw_buffer_store_b128(*st.unit(row, u), rs,
-                                               8 * u < cols ? (int)(2 * (row * ld + 8 * u)) : kPastEnd, 0, 0);
-    }
-}
+};
 
 // The tile of workgroup b of a triangle of Gm x Gm tiles, tm <= tn: consecutive
 // workgroups of an XCD (b mod 8 equal) take neighbouring tiles of one column, so
