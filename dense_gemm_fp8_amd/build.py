@@ -82,11 +82,11 @@ def waterfall_loops(asm: str) -> list[tuple[str, str]]:
     return found
 
 
-def device_asm(out: str) -> None:
-    """Compile the kernels' source to gfx950 assembly (device code only) with
+def device_asm(out: str, source: str = "gemm_kernels.hip") -> None:
+    """Compile a kernel source of csrc/ to gfx950 assembly (device code only) with
     the library's flags, into `out`."""
     cmd = [hipcc(), *HIPCC_FLAGS, "--cuda-device-only", "-S", "-x", "hip",
-           os.path.join(CSRC, "gemm_kernels.hip"), "-I", os.path.join(ROOT, "include"), "-o", out]
+           os.path.join(CSRC, source), "-I", os.path.join(ROOT, "include"), "-o", out]
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + res.stderr[-3000:])

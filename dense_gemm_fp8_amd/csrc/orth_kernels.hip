@@ -296,13 +296,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void orth_small_kernel(const Tile
 {
     __shared__ __attribute__((aligned(1024))) char smem[kSmallWaves * 2 * kSmallPanel];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int tm, tn;
-    if (o.triangle) {
+    int tm = blockIdx.x / o.Gn, tn = blockIdx.x % o.Gn;
+    if (o.triangle)
         triangle_tile(blockIdx.x, o.Gm, tm, tn);
-    } else {
-        tm = blockIdx.x / o.Gn;
-        tn = blockIdx.x % o.Gn;
-    }
     const int row0 = 32 * tm, col0 = 32 * tn, rows = min(32, o.rows_a - row0), cols = min(32, o.rows_b - col0);
     const __amdgpu_buffer_rsrc_t ra = buffer_of(static_cast<const char *>(o.A) + (int64_t)row0 * o.pitch_a,
                                                 panel_range(rows, o.pitch_a, o.kb));

@@ -559,7 +559,8 @@ __device__ __forceinline__ void triangle_tile(int b, int G, int &tm, int &tn)
     const int total = G * (G + 1) / 2, per = total / kNumXcd, whole = per * kNumXcd;
     const int id = b < whole ? (b % kNumXcd) * per + b / kNumXcd : b;
     // column tn holds tiles tn (tn + 1) / 2 .. + tn
-    int c = (int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
+    // (a scalar again: buffers are made from the tile's place)
+    int c = __builtin_amdgcn_readfirstlane((int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f));
     while ((c + 1) * (c + 2) / 2 <= id)
         ++c;
     while (c * (c + 1) / 2 > id)
