@@ -1,5 +1,5 @@
 // orth_api.cpp -- hkg_orthogonalize (hkg_ops.h): argument checks, workspace
-// layout and the launches of its steps.
+// layout and the launches of its steps, single ones or two at a time.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -12,10 +12,11 @@ namespace {
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
 // Byte offsets in the workspace: X [m][np], two X^T [n][mp] (the third product
-// reads one while it writes the other), A and P [m][mp], the norm's partial sums.
+// reads one while it writes the other), three symmetric matrices [m][mp], the norm's
+// partial sums.
 struct OrthLayout {
     int64_t m, n, mp, np;
-    int64_t x, xt[2], a, p, sums, bytes;
+    int64_t x, xt[2], a, p, b, sums, bytes;
 };
 OrthLayout layout(int64_t rows, int64_t cols)
 {
@@ -35,6 +36,7 @@ OrthLayout layout(int64_t rows, int64_t cols)
     l.xt[1] = take(l.n * l.mp);
     l.a = take(l.m * l.mp);
     l.p = take(l.m * l.mp);
+    l.b = take(l.m * l.mp);
     l.sums = at;
     l.bytes = at + round16(8 * hkg::orth_norm_parts());
     return l;
@@ -115,6 +117,21 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
     return hkg::launch_orth_product(128, tiles_of(rest.M, rest.N, p.K, 128), false, rest, re, stream);
 }
 
+// Whether two steps share one pass over X: the second step's A' = X' X'^T is P A P,
+// since P is a polynomial of A, so X'' = (P' P) X needs three symmetric m x m products
+// more and one product over X's n columns and one update less.  Worth it from n = 1.5 m
+// where the update runs on tiles (4096 x 14336: 2574 us against 3368; 4096 x 6144: 1580
+// against 1757; 1024 x 2304: even; 2048 x 2560: 408 against 396; small matrices are bound
+// by their launches, one more here: 256 x 1024 92 us against 86).  P' P, near a^2 where
+// singular values are small, is rounded to fp16 as a whole, which shows next to its
+// smaller values, those of the largest singular values: with these between 1 and 1e-4 a
+// result's singular values end within 0.02 of the exact ones (0.01 by single steps); a
+// larger a takes single steps.
+bool steps_in_pairs(int64_t m, int64_t n, int update_tile, float a)
+{
+    return update_tile != 32 && 2 * n >= 3 * m && a <= 4.0f && a >= -4.0f;
+}
+
 }  // namespace
 }  // namespace hkg::api
 
@@ -170,7 +187,7 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
     const hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     uint16_t *x = reinterpret_cast<uint16_t *>(ws + l.x), *am = reinterpret_cast<uint16_t *>(ws + l.a),
-             *pm = reinterpret_cast<uint16_t *>(ws + l.p);
+             *pm = reinterpret_cast<uint16_t *>(ws + l.p), *bm = reinterpret_cast<uint16_t *>(ws + l.b);
     uint16_t *xt[2] = {reinterpret_cast<uint16_t *>(ws + l.xt[0]), reinterpret_cast<uint16_t *>(ws + l.xt[1])};
     double *sums = reinterpret_cast<double *>(ws + l.sums);
     const hkg::ElemType t = g_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16;
@@ -190,19 +207,30 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
 
     const float s = 1.0f / hkg::kOrthScale;
     const int sym = pick_tile(m, m, true), upd = pick_tile(m, n, false);
-    for (int i = 0; i < steps && rc == HKG_OK; ++i) {
-        const bool last = i + 1 == steps;
-        // A = X X^T
-        rc = launched(hkg::launch_orth_product(sym, tiles_of(m, m, np, sym), true, {x, x, m, m, np},
-                                               {s * s, 0.0f, 0.0f, nullptr, 0, 0, am, mp, mp, am, mp, mp, 0}, st));
-        // P = a I + b A + c A A
+    // out = alpha A B^T + beta D + diag I, symmetric m x m; A and B have rows of K elements
+    auto symmetric = [&](const uint16_t *A, const uint16_t *B, int K, float alpha, float beta, float diag,
+                         const uint16_t *D, uint16_t *to) {
         if (rc == HKG_OK)
             rc = launched(hkg::launch_orth_product(
-                sym, tiles_of(m, m, mp, sym), true, {am, am, m, m, mp},
-                {c, b, a, reinterpret_cast<const _Float16 *>(am), mp, mp, pm, mp, mp, pm, mp, mp, 0}, st));
-        // X <- P X, as X and X^T, or the result in its own orientation
-        hkg::OrthEpilogue ep = {1.0f, 0.0f, 0.0f, nullptr, 0, 0, x, np, np, xt[(i + 1) & 1], mp, mp, 0};
-        if (last) {
+                sym, tiles_of(m, m, K, sym), true, {A, B, m, m, K},
+                {alpha, beta, diag, reinterpret_cast<const _Float16 *>(D), mp, mp, to, mp, mp, to, mp, mp, 0}, st));
+    };
+    const bool pairs = steps_in_pairs(m, n, upd, a);
+    for (int i = 0, xi = 0; i < steps && rc == HKG_OK; ++i, xi ^= 1) {
+        symmetric(x, x, np, s * s, 0.0f, 0.0f, nullptr, am);   // A = X X^T
+        symmetric(am, am, mp, c, b, a, am, pm);                // P = a I + b A + c A A
+        const uint16_t *by = pm;
+        if (pairs && i + 1 < steps) {
+            symmetric(pm, am, mp, 1.0f, 0.0f, 0.0f, nullptr, bm);
+            symmetric(pm, bm, mp, 1.0f, 0.0f, 0.0f, nullptr, am);   // A' = P A P
+            symmetric(am, am, mp, c, b, a, am, bm);                 // P' = a I + b A' + c A' A'
+            symmetric(bm, pm, mp, 1.0f, 0.0f, 0.0f, nullptr, am);   // P' P
+            by = am;
+            ++i;
+        }
+        // X <- P X (or P' P X), as X and X^T, or the result in its own orientation
+        hkg::OrthEpilogue ep = {1.0f, 0.0f, 0.0f, nullptr, 0, 0, x, np, np, xt[xi ^ 1], mp, mp, 0};
+        if (i + 1 == steps) {
             ep = {s, 0.0f, 0.0f, nullptr, 0, 0, nullptr, 0, 0, nullptr, 0, 0, 1};
             if (tall) {
                 ep.transposed = static_cast<uint16_t *>(out);
@@ -215,7 +243,7 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
             }
         }
         if (rc == HKG_OK)
-            rc = launched(launch_update(upd, {pm, xt[i & 1], m, n, mp}, ep, st));
+            rc = launched(launch_update(upd, {by, xt[xi], m, n, mp}, ep, st));
     }
     return rc;
 }

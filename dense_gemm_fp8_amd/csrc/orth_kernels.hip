@@ -15,6 +15,8 @@
 // X is held times 2^12, so that its entries, near 1 / sqrt(m n) at first, stay clear
 // of fp16's subnormals; singular values may then reach 15.  A and P need no scale:
 // what subnormals lose of their small entries (2^-25) is nothing beside a I.
+// Two steps may share the third product (steps_in_pairs, orth_api.cpp): P and A commute,
+// so P A, P (P A) and P' P are symmetric products on the triangle of tiles as well.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

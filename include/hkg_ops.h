@@ -106,8 +106,8 @@ int hkg_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void *x, int32_t x_t
  * where Wt and Xt are the MXFP4 forms of W^T [K][N] and x^T [K][M] (codes_t,
  * packed_t of hkg_mxfp4_quantize_both for operand B).  dy is read once.
  *   dy  bf16 or fp32 (dy_type), rows lddy elements apart (0 = N)
- *   dx, dw  bf16, rows lddx / lddw elements apart (0 = K); either may be NULL
- *           (then its operands may be too)
+ *   dx, dw  bf16, 16-byte aligned, rows lddx / lddw elements apart (0 = K); either
+ *           may be NULL (then its operands may be too)
  */
 int64_t hkg_linear_mxfp4_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, int32_t dy_type,
@@ -127,7 +127,9 @@ int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, i
  *        when both are bf16 with one pitch, else must not overlap it
  *   steps 0 .. 64; eps >= 0 (a zero matrix stays zero)
  * X, A and a I + b A + c A A are kept in fp16 between products (11-bit
- * significands; X scaled by a power of two), sums are fp32; the polynomial must
+ * significands; X scaled by a power of two), sums are fp32.  Where one side is at
+ * least 1.5 times the other (and -4 <= a <= 4) large matrices take two steps on one
+ * pass over X, with A of the second step from that of the first.  The polynomial must
  * keep the singular values of X below 15 (beyond that fp16 overflows to
  * infinity), as the usual coefficients (3.4445, -4.7750, 2.0315) do.  A NaN or an
  * infinity in G makes every element of out NaN.

@@ -185,3 +185,89 @@ def test_every_tile_size_and_the_triangle(rows, cols):
     assert d.norm() <= 0.01 * X.norm()
     tiles = d[:rows // 64 * 64, :cols // 64 * 64].reshape(rows // 64, 64, cols // 64, 64).norm(dim=(1, 3))
     assert tiles.max() <= 0.03 * X.norm() / (rows * cols / 4096) ** 0.5
+
+
+def reference_pairs(G, steps, coeffs=COEFFS, eps=EPS):
+    """(X after `steps` in 64 bits, tolerance of its Frobenius norm).  The roundings'
+    size is what they do in 64 bits with every intermediate of a pair of steps (A, P,
+    B = P A, A' = P B, P', P' P and X, X times 2^12) rounded to fp16; the operator's
+    differ from those in single units by the order of its sums, so it may be off by four
+    times as much, plus the bf16 rounding of the result."""
+    a, b, c = coeffs
+    G = np.asarray(G, dtype=np.float64)
+    tall = G.shape[0] > G.shape[1]
+    X = (G.T if tall else G) / (np.linalg.norm(G) + eps)
+    eye = np.eye(X.shape[0])
+
+    def fp16(M, scale=1.0):
+        return (M * scale).astype(np.float16).astype(np.float64) / scale
+
+    Y, left = fp16(X, 4096.0), steps
+    for _ in range(steps):
+        A = X @ X.T
+        X = (a * eye + b * A + c * (A @ A)) @ X
+    while left:
+        A = fp16(Y @ Y.T)
+        Q = fp16(a * eye + b * A + c * (A @ A))
+        if left >= 2:
+            A2 = fp16(Q @ fp16(Q @ A))
+            Q = fp16(fp16(a * eye + b * A2 + c * (A2 @ A2)) @ Q)
+        Y = fp16(Q @ Y, 4096.0)
+        left -= min(left, 2)
+    tol = 4 * np.linalg.norm(Y - X) + 2.0 ** -8 * np.linalg.norm(X)
+    return (X.T if tall else X), tol
+
+
+def check_pairs(out, G, **kw):
+    want, tol = reference_pairs(G.double().numpy(), **kw)
+    got = host(out)
+    off = np.linalg.norm(got - want)
+    assert np.isfinite(got).all() and off <= tol, "%g off, %g allowed, of %g" % (off, tol, np.linalg.norm(want))
+    each = 8 * tol / np.sqrt(want.size) + 2.0 ** -8 * np.abs(want)
+    assert (np.abs(got - want) <= each).all()
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("rows,cols", [(700, 4500), (4500, 701)])
+def test_steps_in_pairs(rows, cols, steps):
+    print("orth pairs %dx%d %d" % (rows, cols, steps), flush=True)
+    G = gradient(7 * steps, rows, cols)
+    check_pairs(hkg.orthogonalize(G.cuda(), steps=steps), G, steps=steps)
+
+
+@pytest.mark.parametrize("rows,cols", [(1500, 2250), (1500, 2249), (2249, 1500), (2250, 1500), (130, 18000)])
+def test_steps_in_pairs_from_where_they_start(rows, cols):
+    G = gradient(8, rows, cols, torch.bfloat16)
+    check_pairs(hkg.orthogonalize(G.cuda()), G, steps=5)
+
+
+@pytest.mark.parametrize("coeffs,steps", [((4.0, -6.0, 2.5), 3), ((4.5, -6.0, 2.0), 2), ((-3.0, 4.0, -1.5), 4), ((1.5, -0.5, 0.0), 20)])
+def test_steps_in_pairs_other_coefficients(coeffs, steps):
+    """a = 4.5 takes single steps, whose error budget is below that of pairs."""
+    G = gradient(9, 640, 4500)
+    check_pairs(hkg.orthogonalize(G.cuda(), steps=steps, coefficients=coeffs), G, steps=steps, coeffs=coeffs)
+
+
+def test_steps_in_pairs_with_small_singular_values():
+    # singular values from 1 to 1e-4: those of the result, by the step's own polynomial
+    g = torch.Generator().manual_seed(10)
+    U = torch.linalg.qr(torch.randn(640, 640, generator=g, dtype=torch.float64))[0]
+    V = torch.linalg.qr(torch.randn(4500, 640, generator=g, dtype=torch.float64))[0]
+    G = ((U * torch.logspace(0, -4, 640, dtype=torch.float64)) @ V.t()).float()
+    s = torch.linalg.svdvals(G.double())
+    s = s / s.norm()
+    for _ in range(5):
+        s = COEFFS[0] * s + COEFFS[1] * s ** 3 + COEFFS[2] * s ** 5
+    got = torch.diagonal(U.t() @ hkg.orthogonalize(G.cuda()).cpu().double() @ V)
+    check_pairs(hkg.orthogonalize(G.cuda()), G, steps=5)
+    assert (got - s).abs().max() <= 0.05
+
+
+def test_steps_in_pairs_repeat_and_ignore_their_workspace():
+    G = gradient(11, 700, 4500).cuda()
+    need = ops._lib().hkg_orthogonalize_workspace_bytes(700, 4500)
+    want = hkg.orthogonalize(G)
+    for fill in (0, 0x7C, 0xFF):
+        ws = torch.full((need + 512,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(hkg.orthogonalize(G, workspace=ws[:need]), want)
+        assert (ws[need:] == fill).all()
