@@ -17,7 +17,9 @@ namespace {
 // Along K: a lane holds 8 consecutive elements, a quad of lanes one block, so a
 // wave reads 4 rows of 256 or 512 bytes at once and two DPP steps give a
 // block's largest magnitude.  Along rows: the tile is staged in LDS, a wave
-// takes 32 of its rows and a lane 2 columns, one after the other.
+// takes 32 of its rows and a lane 2 columns, one after the other.  Bound by its
+// bytes: both forms of 14336 x 4096 fp32 (235 MB read, 62 written) in 68 us, 4.4 TB/s,
+// of 8192 x 14336 bf16 (235 and 125) in 84 us, 4.3 TB/s; a 2 GiB copy reaches 4.9.
 constexpr int kQTile = 128;
 
 template <int kElem, bool kBoth>
@@ -111,7 +113,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const QuantParams p)
 }
 
 // ---- the values of an MXFP4 matrix ------------------------------------------
-// A lane turns one word of codes (8 elements) into 16 or 32 bytes.
+// A lane turns one word of codes (8 elements) into 16 or 32 bytes.  Bound by its
+// bytes: 14336 x 4096 to bf16 (31 MB read, 117 written) in 31 us, 4.8 TB/s.
 template <int kElem>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams p)
 {

@@ -162,6 +162,10 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
 }
 
 // ---- a product of a step -----------------------------------------------------
+// Bound by the matrix cores at the clock the power cap leaves: X <- P X at 4096 x 14336
+// 384 us (1253 TFLOPS at 1.86 GHz, the cores busy 67 % of the whole launch), the
+// triangle of a 4096^2 product 66 us over K = 4096 and 202 us over K = 14336 (253
+// 192-tiles on 256 compute units).
 // v = alpha acc + beta D, stored as rows (straight) and/or as columns (transposed),
 // both through a staged quarter of the tile (tile16.h): D is loaded into it, each
 // lane replaces D's units by its results, and whole runs of rows or of columns leave.
