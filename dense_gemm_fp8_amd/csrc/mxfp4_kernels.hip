@@ -121,52 +121,54 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams
     const int words = p.kp / 8, nk = (p.kp + kMxStep - 1) / kMxStep;
     const int cols = (words + 63) / 64;           // workgroups per 4 rows
     const int w = blockIdx.x % cols * 64 + (threadIdx.x & 63);
-    const int row = blockIdx.x / cols * 4 + (threadIdx.x >> 6);
-    if (w >= words || row >= p.rows)
+    if (w >= words)
         return;
-    const uint32_t q = *reinterpret_cast<const uint32_t *>(p.codes + (int64_t)row * (p.kp / 2) + 4 * w);
-    const int blk = w >> 2;
-    const uint32_t code = p.packed[((int64_t)(row >> 7) * nk + (blk >> 2)) * kMxStepScales +
-                                   scale_byte(p.operand, row & 127, blk & 3)];
-    const float s = scale_operand(code);
-    const bool nan = code == kScaleNan;
-    const int64_t at = (int64_t)row * p.ldv + 8 * w;
-    const bool vec = ((reinterpret_cast<uintptr_t>(p.values) | (uintptr_t)(p.ldv * (kElem == 0 ? 2 : 4))) & 15) == 0;
-    if constexpr (kElem == 0) {
-        u32x4_t o;
-        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
-        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
-        o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
-        o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
+    const int64_t stride = gridDim.x / cols * 4;
+    for (int64_t row = blockIdx.x / cols * 4 + (threadIdx.x >> 6); row < p.rows; row += stride) {
+        const uint32_t q = *reinterpret_cast<const uint32_t *>(p.codes + row * (p.kp / 2) + 4 * w);
+        const int blk = w >> 2;
+        const uint32_t code = p.packed[((int64_t)(row >> 7) * nk + (blk >> 2)) * kMxStepScales +
+                                       scale_byte(p.operand, (int)row & 127, blk & 3)];
+        const float s = scale_operand(code);
+        const bool nan = code == kScaleNan;
+        const int64_t at = row * p.ldv + 8 * w;
+        const bool vec = ((reinterpret_cast<uintptr_t>(p.values) | (uintptr_t)(p.ldv * (kElem == 0 ? 2 : 4))) & 15) == 0;
+        if constexpr (kElem == 0) {
+            u32x4_t o;
+            o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0));
+            o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1));
+            o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2));
+            o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = nan ? 0x7fc07fc0u : o[i];
-        uint16_t *d = static_cast<uint16_t *>(p.values) + at;
-        if (vec)
-            *reinterpret_cast<u32x4_t *>(d) = o;
-        else
+            for (int i = 0; i < 4; ++i)
+                o[i] = nan ? 0x7fc07fc0u : o[i];
+            uint16_t *d = static_cast<uint16_t *>(p.values) + at;
+            if (vec)
+                *reinterpret_cast<u32x4_t *>(d) = o;
+            else
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                d[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-    } else {
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        uint32_t o[8];
-        const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
-        const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
-        const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
-        const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
-        const float f[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = nan ? 0x7fc00000u : __builtin_bit_cast(uint32_t, f[i]);
-        uint32_t *d = static_cast<uint32_t *>(p.values) + at;
-        if (vec) {
-            *reinterpret_cast<u32x4_t *>(d) = u32x4_t{o[0], o[1], o[2], o[3]};
-            *reinterpret_cast<u32x4_t *>(d + 4) = u32x4_t{o[4], o[5], o[6], o[7]};
+                for (int i = 0; i < 8; ++i)
+                    d[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
         } else {
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            uint32_t o[8];
+            const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
+            const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
+            const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
+            const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
+            const float f[8] = {a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                d[i] = o[i];
+                o[i] = nan ? 0x7fc00000u : __builtin_bit_cast(uint32_t, f[i]);
+            uint32_t *d = static_cast<uint32_t *>(p.values) + at;
+            if (vec) {
+                *reinterpret_cast<u32x4_t *>(d) = u32x4_t{o[0], o[1], o[2], o[3]};
+                *reinterpret_cast<u32x4_t *>(d + 4) = u32x4_t{o[4], o[5], o[6], o[7]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[i] = o[i];
+            }
         }
     }
 }
@@ -432,7 +434,10 @@ hipError_t launch_mx4_quantize(ElemType t, const QuantParams &p, hipStream_t str
 
 hipError_t launch_mx4_dequantize(ElemType t, const DequantParams &p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((p.kp / 8 + 63) / 64) * ((p.rows + 3) / 4)), block(256);
+    // at most 2^23 workgroups, so that their threads stay below 2^32; the rest of a
+    // very long matrix in turns
+    const unsigned cols = (p.kp / 8 + 63) / 64, quads = (p.rows + 3) / 4, most = (1u << 23) / cols;
+    const dim3 grid(cols * (quads < most ? quads : most)), block(256);
     if (t == kElemBf16)
         hipLaunchKernelGGL(mx4_dequantize_kernel<0>, grid, block, 0, stream, p);
     else

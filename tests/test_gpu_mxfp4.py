@@ -409,3 +409,35 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for got, want in zip(out, step()):
             np.testing.assert_array_equal(bits(got), bits(want))
+
+
+def test_offsets_past_32_bits():
+    """40 000 000 rows of 64: elements of x, values and C lie past 2^31, bytes past 2^32, and
+    the dequantising launch takes its rows in turns.  Row r is one pattern of exact
+    values times 2^(r mod 7), so every result is known."""
+    rows, K, N = 40_000_000, 64, 64
+    g = np.random.Generator(np.random.PCG64(5))
+    pattern = ref.MAGNITUDES[g.integers(0, 8, size=K)] * g.choice([-1.0, 1.0], size=K)
+    pattern[[0, 40]] = 6.0                               # both blocks' scales: the row's power
+    seven = pattern[None, :] * 2.0 ** np.arange(7)[:, None]
+    some = torch.from_numpy(seven).to(torch.bfloat16).cuda()
+    period = some.repeat(100_000, 1)                     # 700 000 rows, a multiple of 7
+    x = torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
+
+    def parts(t):
+        for r in range(0, rows, len(period)):
+            yield t[r:r + len(period)]
+
+    for part in parts(x):
+        part.copy_(period[:len(part)])
+    codes, packed = hkg.mxfp4_quantize(x, A)
+    v = hkg.mxfp4_dequantize(codes, packed, A)
+    assert all(torch.equal(a, b) for a, b in zip(parts(v), parts(x)))
+    del v, x
+    w = ref.MAGNITUDES[g.integers(0, 8, size=(N, K))] * g.choice([-1.0, 1.0], size=(N, K))
+    w[:, [0, 40]] = 6.0
+    wc, ws = hkg.mxfp4_quantize(torch.from_numpy(w).float().cuda(), B)
+    C = hkg.gemm_mxfp4(codes, wc, packed, ws)
+    # sums of 64 products in steps of 1/4 below 64 * 36: exact in fp32, rounded once
+    want = torch.from_numpy(seven @ w.T).float().to(torch.bfloat16).cuda().repeat(100_000, 1)
+    assert all(torch.equal(part, want[:len(part)]) for part in parts(C))
