@@ -1,5 +1,5 @@
 // orth_api.cpp -- hkg_orthogonalize (hkg_ops.h): argument checks, workspace
-// layout and the launches of its steps, single ones or two at a time.
+// layout and the launches of its steps.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -11,12 +11,24 @@ namespace {
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// Byte offsets in the workspace: X [m][np], two X^T [n][mp] (the third product
-// reads one while it writes the other), three symmetric matrices [m][mp], the norm's
-// partial sums.
+// Up to so many 32 x 32 blocks a product runs on the kernel for small matrices (five
+// steps on it against five on tiles: 256 x 256 67 us against 116, 1024 x 2048 -- 2048
+// blocks in its third product -- 211 against 250 without with_low's addition, 2048 x
+// 2048 866 against 354).
+constexpr int64_t kSmallBlocks = 2048;
+
+// Whether X X^T takes what fp16 leaves out of X too: where every product runs on the
+// kernel for small matrices, bound by latency, and K is short.  768 x 768 130 us, 118 without;
+// 1024 x 2048 259 and 211; 64 x 14336, which is beyond the rule, would take 262 and
+// takes 163.  On tiles it would cost X X^T twice over.
+bool with_low(int64_t mp, int64_t np) { return (mp / 32) * (np / 32) <= kSmallBlocks && np <= 2048; }
+
+// Byte offsets in the workspace: X in fp32 (OrthState), its fp16 forms X [m][xp] and two
+// X^T [n][mp] (the third product reads one while it writes the other), two symmetric
+// matrices [m][mp] with their diagonals in fp32, the norm's partial sums.
 struct OrthLayout {
-    int64_t m, n, mp, np;
-    int64_t x, xt[2], a, p, b, sums, bytes;
+    int64_t m, n, mp, np, xp;
+    int64_t state, x, xt[2], a, b, da, db, sums, bytes;
 };
 OrthLayout layout(int64_t rows, int64_t cols)
 {
@@ -25,18 +37,21 @@ OrthLayout layout(int64_t rows, int64_t cols)
     l.n = rows < cols ? cols : rows;
     l.mp = pad64(l.m);
     l.np = pad64(l.n);
+    l.xp = with_low(l.mp, l.np) ? 2 * l.np : l.np;
     int64_t at = 0;
-    auto take = [&](int64_t elems) {
+    auto take = [&](int64_t elems, int64_t size) {
         const int64_t here = at;
-        at += 2 * elems;         // rows of 128 bytes: every part stays aligned
+        at += size * elems;      // multiples of 64 elements: every part stays aligned
         return here;
     };
-    l.x = take(l.m * l.np);
-    l.xt[0] = take(l.n * l.mp);
-    l.xt[1] = take(l.n * l.mp);
-    l.a = take(l.m * l.mp);
-    l.p = take(l.m * l.mp);
-    l.b = take(l.m * l.mp);
+    l.state = take(l.mp * l.np, 4);
+    l.x = take(l.m * l.xp, 2);
+    l.xt[0] = take(l.n * l.mp, 2);
+    l.xt[1] = take(l.n * l.mp, 2);
+    l.a = take(l.m * l.mp, 2);
+    l.b = take(l.m * l.mp, 2);
+    l.da = take(l.mp, 4);
+    l.db = take(l.mp, 4);
     l.sums = at;
     l.bytes = at + round16(8 * hkg::orth_norm_parts());
     return l;
@@ -48,11 +63,6 @@ bool sizes_fit(int64_t rows, int64_t cols)
     constexpr int64_t kMax = (int64_t(1) << 31) / (256 * 2) - 64;
     return rows <= kMax && cols <= kMax;
 }
-
-// Up to so many 32 x 32 blocks a product runs on the kernel for small matrices (five
-// steps on it against five on tiles: 256 x 256 68 us against 108, 1024 x 2048 -- 2048
-// blocks in its third product -- 213 against 236, 2048 x 2048 665 against 336).
-constexpr int64_t kSmallBlocks = 2048;
 
 // The tile of a product (M x N, or the triangle of an M x M): the one whose rounds
 // of the 256 compute units take least, a unit's time for a tile growing with its
@@ -86,7 +96,7 @@ hkg::TileOrder tiles_of(int64_t M, int64_t N, int64_t K, int tile)
     return order_of(pad64(M), pad64(N), 2 * K, tile);
 }
 
-// X <- P X (m x n), whole or in the two parts of split_last_round.
+// The update of X (m x n), whole or in the two parts of split_last_round.
 hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpilogue &e, hipStream_t stream)
 {
     const TileSplit split = tile == 256 ? split_last_round(p.M, p.N) : TileSplit{0, false};
@@ -103,6 +113,9 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
         re.straight += e.straight ? keep * e.lds : 0;
         re.transposed += e.transposed ? keep : 0;
         re.cols_t -= keep;
+        re.state.x += keep / 16 * e.state.pitch;
+        re.d += keep;
+        re.rows_d -= keep;
     } else {
         head.N = keep;
         rest.N -= keep;
@@ -110,26 +123,13 @@ hipError_t launch_update(int tile, const hkg::OrthProduct &p, const hkg::OrthEpi
         re.straight += e.straight ? keep : 0;
         re.cols_s -= keep;
         re.transposed += e.transposed ? keep * e.ldt : 0;
+        re.state.x += keep / 32 * hkg::kOrthBlock;
+        re.state.blocks -= keep / 32;
     }
     const hipError_t err = hkg::launch_orth_product(256, tiles_of(head.M, head.N, p.K, 256), false, head, e, stream);
     if (err != hipSuccess)
         return err;
     return hkg::launch_orth_product(128, tiles_of(rest.M, rest.N, p.K, 128), false, rest, re, stream);
-}
-
-// Whether two steps share one pass over X: the second step's A' = X' X'^T is P A P,
-// since P is a polynomial of A, so X'' = (P' P) X needs three symmetric m x m products
-// more and one product over X's n columns and one update less.  Worth it from n = 1.5 m
-// where the update runs on tiles (4096 x 14336: 2574 us against 3368; 4096 x 6144: 1580
-// against 1757; 1024 x 2304: even; 2048 x 2560: 408 against 396; small matrices are bound
-// by their launches, one more here: 256 x 1024 92 us against 86).  P' P, near a^2 where
-// singular values are small, is rounded to fp16 as a whole, which shows next to its
-// smaller values, those of the largest singular values: with these between 1 and 1e-4 a
-// result's singular values end within 0.02 of the exact ones (0.01 by single steps); a
-// larger a takes single steps.
-bool steps_in_pairs(int64_t m, int64_t n, int update_tile, float a)
-{
-    return update_tile != 32 && 2 * n >= 3 * m && a <= 4.0f && a >= -4.0f;
 }
 
 }  // namespace
@@ -186,64 +186,73 @@ int hkg_orthogonalize(int64_t rows, int64_t cols, const void *G, int32_t g_type,
 
     const hipStream_t st = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    uint16_t *x = reinterpret_cast<uint16_t *>(ws + l.x), *am = reinterpret_cast<uint16_t *>(ws + l.a),
-             *pm = reinterpret_cast<uint16_t *>(ws + l.p), *bm = reinterpret_cast<uint16_t *>(ws + l.b);
-    uint16_t *xt[2] = {reinterpret_cast<uint16_t *>(ws + l.xt[0]), reinterpret_cast<uint16_t *>(ws + l.xt[1])};
+    auto half = [&](int64_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
+    auto full = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
+    uint16_t *const x = half(l.x), *const xt[2] = {half(l.xt[0]), half(l.xt[1])}, *const am = half(l.a), *const bm = half(l.b);
+    float *const da = full(l.da), *const db = full(l.db);
     double *sums = reinterpret_cast<double *>(ws + l.sums);
     const hkg::ElemType t = g_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16;
     const hkg::OrthInput in = {G, ldg, static_cast<int>(rows), static_cast<int>(cols)};
     const bool tall = rows > cols;
     const int m = static_cast<int>(l.m), n = static_cast<int>(l.n), mp = static_cast<int>(l.mp),
-              np = static_cast<int>(l.np);
+              np = static_cast<int>(l.np), xp = static_cast<int>(l.xp), low = xp - np;
 
     rc = launched(hkg::launch_orth_norm(t, in, sums, st));
     if (rc != HKG_OK)
         return rc;
     if (steps == 0)
-        return launched(hkg::launch_orth_convert(t, in, sums, eps, nullptr, 0, nullptr, 0,
+        return launched(hkg::launch_orth_convert(t, in, sums, eps, {}, nullptr, 0, nullptr, 0, 0,
                                                  static_cast<uint16_t *>(out), ldo, st));
-    rc = launched(tall ? hkg::launch_orth_convert(t, in, sums, eps, xt[0], mp, x, np, nullptr, 0, st)
-                       : hkg::launch_orth_convert(t, in, sums, eps, x, np, xt[0], mp, nullptr, 0, st));
+    const hkg::OrthState state = {full(l.state), 16 * l.np, np / 32};
+    rc = launched(tall ? hkg::launch_orth_convert(t, in, sums, eps, state, xt[0], mp, x, xp, low, nullptr, 0, st)
+                       : hkg::launch_orth_convert(t, in, sums, eps, state, x, xp, xt[0], mp, low, nullptr, 0, st));
 
     const float s = 1.0f / hkg::kOrthScale;
     const int sym = pick_tile(m, m, true), upd = pick_tile(m, n, false);
-    // out = alpha A B^T + beta D + diag I, symmetric m x m; A and B have rows of K elements
-    auto symmetric = [&](const uint16_t *A, const uint16_t *B, int K, float alpha, float beta, float diag,
-                         const uint16_t *D, uint16_t *to) {
+    // from rows of K elements: to = gamma (from from^T) alone (D null), or with D = from
+    // and its diagonal r beta S + gamma S S for their matrix S; the diagonal to diag
+    auto symmetric = [&](const uint16_t *from, int K, float gamma, float beta, const uint16_t *D, const float *r,
+                         uint16_t *to, float *diag) {
+        hkg::OrthEpilogue ep = {};
+        ep.gamma = gamma;
+        ep.beta = beta;
+        ep.D = reinterpret_cast<const _Float16 *>(D);
+        ep.r = r;
+        ep.diag = diag;
+        ep.straight = ep.transposed = to;
+        ep.ldd = ep.lds = ep.ldt = ep.cols_d = ep.cols_s = ep.cols_t = mp;
         if (rc == HKG_OK)
-            rc = launched(hkg::launch_orth_product(
-                sym, tiles_of(m, m, K, sym), true, {A, B, m, m, K},
-                {alpha, beta, diag, reinterpret_cast<const _Float16 *>(D), mp, mp, to, mp, mp, to, mp, mp, 0}, st));
+            rc = launched(hkg::launch_orth_product(sym, tiles_of(m, m, K, sym), true, {from, from, m, m, K, !D && low > 0}, ep, st));
     };
-    const bool pairs = steps_in_pairs(m, n, upd, a);
-    for (int i = 0, xi = 0; i < steps && rc == HKG_OK; ++i, xi ^= 1) {
-        symmetric(x, x, np, s * s, 0.0f, 0.0f, nullptr, am);   // A = X X^T
-        symmetric(am, am, mp, c, b, a, am, pm);                // P = a I + b A + c A A
-        const uint16_t *by = pm;
-        if (pairs && i + 1 < steps) {
-            symmetric(pm, am, mp, 1.0f, 0.0f, 0.0f, nullptr, bm);
-            symmetric(pm, bm, mp, 1.0f, 0.0f, 0.0f, nullptr, am);   // A' = P A P
-            symmetric(am, am, mp, c, b, a, am, bm);                 // P' = a I + b A' + c A' A'
-            symmetric(bm, pm, mp, 1.0f, 0.0f, 0.0f, nullptr, am);   // P' P
-            by = am;
-            ++i;
-        }
-        // X <- P X (or P' P X), as X and X^T, or the result in its own orientation
-        hkg::OrthEpilogue ep = {1.0f, 0.0f, 0.0f, nullptr, 0, 0, x, np, np, xt[xi ^ 1], mp, mp, 0};
-        if (i + 1 == steps) {
-            ep = {s, 0.0f, 0.0f, nullptr, 0, 0, nullptr, 0, 0, nullptr, 0, 0, 1};
-            if (tall) {
-                ep.transposed = static_cast<uint16_t *>(out);
-                ep.ldt = ldo;
-                ep.cols_t = m;
-            } else {
-                ep.straight = static_cast<uint16_t *>(out);
-                ep.lds = ldo;
-                ep.cols_s = n;
-            }
+    for (int i = 0; i < steps && rc == HKG_OK; ++i) {
+        symmetric(x, np, s * s, 0.0f, nullptr, nullptr, am, da);   // A = X X^T
+        symmetric(am, mp, c, b, am, da, bm, db);                   // B = b A + c A A
+        // X <- a X + B X, as X and X^T, or the result in its own orientation
+        hkg::OrthEpilogue ep = {};
+        ep.gamma = s;
+        ep.state = state;
+        ep.a = a;
+        ep.d = db;
+        ep.rows_d = mp;
+        ep.last = i + 1 == steps;
+        if (!ep.last) {
+            ep.straight = x;
+            ep.lds = xp;
+            ep.cols_s = np;
+            ep.low = low;
+            ep.transposed = xt[(i & 1) ^ 1];
+            ep.ldt = ep.cols_t = mp;
+        } else if (tall) {
+            ep.transposed = static_cast<uint16_t *>(out);
+            ep.ldt = ldo;
+            ep.cols_t = m;
+        } else {
+            ep.straight = static_cast<uint16_t *>(out);
+            ep.lds = ldo;
+            ep.cols_s = n;
         }
         if (rc == HKG_OK)
-            rc = launched(launch_update(upd, {by, xt[xi], m, n, mp}, ep, st));
+            rc = launched(launch_update(upd, {bm, xt[i & 1], m, n, mp, false}, ep, st));
     }
     return rc;
 }
