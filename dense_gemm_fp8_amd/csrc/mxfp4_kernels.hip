@@ -393,6 +393,18 @@ __device__ __forceinline__ void mx4_few_rows(const Mx4GemmParams &p, int block, 
     }
 }
 
+// ---- the product without K ----------------------------------------------------
+// Workgroups take 256 columns of a row, in turns in both directions.
+__global__ __launch_bounds__(256) void mx4_zero_kernel(const Mx4GemmParams p)
+{
+    for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y)
+        for (int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x; col < p.N; col += (int64_t)gridDim.x * 256) {
+            p.C[row * p.ldc + col] = 0;
+            if (p.C_f32)
+                p.C_f32[row * p.ldc + col] = 0.0f;
+        }
+}
+
 template <int kXt, int kMb, int kS>
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(const Mx4GemmParams p)
 {
@@ -460,6 +472,14 @@ static bool two_steps(unsigned blocks, int K) { return blocks <= 256 || K >= 819
 static unsigned few_blocks(const Mx4GemmParams &p, int mb)
 {
     return (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
+}
+
+hipError_t launch_mx4_zero(const Mx4GemmParams &p, hipStream_t stream)
+{
+    const int64_t cols = ((int64_t)p.N + 255) / 256;
+    const dim3 grid((unsigned)(cols < 256 ? cols : 256), (unsigned)(p.M < 4096 ? p.M : 4096));
+    hipLaunchKernelGGL(mx4_zero_kernel, grid, dim3(256), 0, stream, p);
+    return hipGetLastError();
 }
 
 hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream)

@@ -106,6 +106,8 @@ int product_tile(const hkg::Mx4GemmParams &p)   // 0: the kernel for few rows
 hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
 {
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (p.K == 0)
+        return hkg::launch_mx4_zero(p, st);
     const int tile = product_tile(p);
     if (tile == 0)
         return hkg::launch_mx4_few_rows(hkg::kElemBf16, p, st);
@@ -130,7 +132,7 @@ hipError_t run_product(const hkg::Mx4GemmParams &p, void *stream)
     return hkg::launch_mx4_tiles(128, order_of(rest.M, rest.N, p.kb, 128), rest, st);
 }
 
-// Two independent products, in one launch where both take the same kernel: a launch less
+// Two independent products (K > 0 in both), in one launch where both take the same kernel: a launch less
 // for small ones (the gradients of 500 x 1000 x 768: 17.2 us against 20.8), one partial
 // last round instead of two for large ones, the longer tiles first (8192 x 14336 x 4096:
 // 484 us against 490).
@@ -287,7 +289,7 @@ int hkg_linear_mxfp4(int64_t M, int64_t N, int64_t K, const void *x, int32_t x_t
         return rc;
     const hkg::ElemType t = x_type == HKG_T_F32 ? hkg::kElemF32 : hkg::kElemBf16;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (need == 0) {
+    if (need == 0 && K > 0) {
         hkg::Mx4GemmParams p = product(M, N, K, nullptr, nullptr, W, SW, y, nullptr, ldy);
         p.x = x;
         p.ldx = ldx;

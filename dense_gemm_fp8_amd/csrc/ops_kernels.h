@@ -42,6 +42,9 @@ struct Mx4GemmParams {
     int64_t ldc;
     int M, N, K, kb;
 };
+// K = 0: C and C_f32 are zeros, whatever the operands.
+hipError_t launch_mx4_zero(const Mx4GemmParams &p, hipStream_t stream);
+// K > 0 from here on.
 hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream);
 // Two products in one launch (both A's are codes).
 hipError_t launch_mx4_few_rows2(const Mx4GemmParams &p, const Mx4GemmParams &p2, hipStream_t stream);

@@ -181,7 +181,8 @@ constexpr bool plan_ok()
 }
 static_assert(plan_ok<8>() && plan_ok<6>() && plan_ok<4>(), "slot plans");
 
-// Runs the K loop of tile (tm, tn) into acc; smem: 5 panels.  On return every load
+// Runs the K loop of tile (tm, tn) into acc; smem: 5 panels, nk at least 1 (its first
+// loads, and those of the scales, are not guarded).  On return every load
 // of this wave has landed; other waves may still be reading their last fragments.
 template <class Mma, int kT>
 struct TileLoop {
