@@ -12,14 +12,17 @@ codes a byte (Kp = K rounded up to 32) and its E8M0 scales in packed order.
     y = linear_mxfp4(X, w, sw)                           # serving, from one row up
 
 with A, B = HKG_MX_OPERAND_A, HKG_MX_OPERAND_B.  Every function takes `stream`
-(default: torch's current one) and enqueues its work there; outputs and
-workspaces it allocates belong to that stream.  A failed check raises
-HkgError with the library's status (ValueError / TypeError for tensors of the
-wrong kind); nothing has run then.
+(default: torch's current one on the tensors' GPU, whichever GPU is current) and
+enqueues its work there; outputs and workspaces it allocates belong to that
+stream.  All tensors of a call, and the stream, are on one GPU.  A failed check
+raises HkgError with the library's status (ValueError / TypeError for tensors of
+the wrong kind); nothing has run then.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 
 import dense_gemm_fp8_amd as _hkg
 
@@ -125,10 +128,35 @@ def _dense(t, name):
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else _hkg._dev_ptr(t, name)
 
 
-def _handle(stream, t) -> int:
-    """Handle of the stream a call runs on: `stream`, or torch's current one on t's device."""
+def _on_its_device(f):
+    """f with the GPU of its first tensor current, which the launches need: the
+    handle of a device's default stream is 0, and stands for the current device's."""
+    first = next(iter(inspect.signature(f).parameters))
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        import torch
+        t = args[0] if args else kw.get(first)
+        if not getattr(t, "is_cuda", False) or t.get_device() == torch.cuda.current_device():
+            return f(*args, **kw)
+        with torch.cuda.device(t.get_device()):
+            return f(*args, **kw)
+    return call
+
+
+def _handle(stream, t, *others) -> int:
+    """Handle of the stream a call runs on: `stream`, or torch's current one on t's
+    device; `others`: the call's other tensors, or None."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one GPU")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("stream must belong to the tensors' GPU")
+        return int(stream.cuda_stream)
     _lib()
-    return int(stream.cuda_stream) if stream is not None else _raw_stream(t.get_device())
+    return _raw_stream(dev)
 
 
 def _empty(shape, dtype, like, stream):
@@ -166,6 +194,7 @@ def _workspace(t, need, like, stream):
     return t, _hkg._dev_ptr(t, "workspace"), t.numel() * t.element_size()
 
 
+@_on_its_device
 def mxfp4_quantize(x, operand, stream=None):
     """MXFP4 form of x [rows, K] (bf16 or fp32, rows contiguous) along K ->
     (codes [rows, Kp / 2], packed scales for `operand`)."""
@@ -181,6 +210,7 @@ def mxfp4_quantize(x, operand, stream=None):
     return codes, packed
 
 
+@_on_its_device
 def mxfp4_quantize_both(x, operand, operand_t, stream=None):
     """mxfp4_quantize(x) and, from the same pass over x, the MXFP4 form of x^T
     -> (codes, packed, codes_t [K, Rp / 2], packed_t)."""
@@ -199,6 +229,7 @@ def mxfp4_quantize_both(x, operand, operand_t, stream=None):
     return codes, packed, codes_t, packed_t
 
 
+@_on_its_device
 def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     """The values of an MXFP4 matrix, [rows, Kp] in bf16 (default) or fp32."""
     import torch
@@ -208,7 +239,7 @@ def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     if K % 32:
         raise ValueError("codes must hold whole blocks of 32 (16 bytes a row)")
     pc, pp = _codes(codes, rows, K, "codes"), _packed(packed, rows, K, "packed")
-    st = _handle(stream, codes)
+    st = _handle(stream, codes, packed, out)
     dtype = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
     out, po, ld = _output(out, (rows, K), dtype, "out", codes, stream)
     _check(_lib().hkg_mxfp4_dequantize(operand, rows, K, pc, pp, po, _elem_type(out, "out"), ld,
@@ -216,6 +247,7 @@ def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     return out
 
 
+@_on_its_device
 def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
     """C[M,N] (bf16) = A[M,K] · B[N,K]ᵀ of two MXFP4 matrices; returns C."""
     import torch
@@ -226,7 +258,7 @@ def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
         raise ValueError("A and B must hold whole blocks of 32 (16 bytes a row)")
     pa, pb = _codes(A, M, K, "A"), _codes(B, N, K, "B")
     sa, sb = _packed(SA_packed, M, K, "SA_packed"), _packed(SB_packed, N, K, "SB_packed")
-    st = _handle(stream, A)
+    st = _handle(stream, A, B, SA_packed, SB_packed, C, C_f32)
     C, pc, ldc = _output(C, (M, N), torch.bfloat16, "C", A, stream)
     pf = None
     if C_f32 is not None:
@@ -237,6 +269,7 @@ def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
     return C
 
 
+@_on_its_device
 def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     """y[M,N] (bf16) = Q(x)[M,K] · W[N,K]ᵀ with x quantised to MXFP4 on the way
     (x bf16 or fp32; W, SW_packed an MXFP4 matrix packed for operand B).
@@ -247,7 +280,7 @@ def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     M, K = x.shape
     N = W.shape[0]
     pw, ps = _codes(W, N, K, "W"), _packed(SW_packed, N, K, "SW_packed")
-    st = _handle(stream, x)
+    st = _handle(stream, x, W, SW_packed, y, workspace)
     y, py, ldy = _output(y, (M, N), torch.bfloat16, "y", x, stream)
     need = _check(_lib().hkg_linear_mxfp4_workspace_bytes(M, N, K), "hkg_linear_mxfp4_workspace_bytes")
     workspace, pws, nws = _workspace(workspace, need, x, stream)
@@ -256,6 +289,7 @@ def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     return y
 
 
+@_on_its_device
 def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, workspace=None,
                           stream=None):
     """Gradients of y = Q(x) Wᵀ, rounding passed straight through: (dx [M,K], dw
@@ -268,7 +302,7 @@ def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, 
     K = Wt.shape[0]
     pw, psw = _codes(Wt, K, N, "Wt"), _packed(SWt_packed, K, N, "SWt_packed")
     px, psx = _codes(Xt, K, M, "Xt"), _packed(SXt_packed, K, M, "SXt_packed")
-    st = _handle(stream, dy)
+    st = _handle(stream, dy, Wt, SWt_packed, Xt, SXt_packed, dx, dw, workspace)
     dx, pdx, lddx = _output(dx, (M, K), torch.bfloat16, "dx", dy, stream)
     dw, pdw, lddw = _output(dw, (N, K), torch.bfloat16, "dw", dy, stream)
     need = _check(_lib().hkg_linear_mxfp4_backward_workspace_bytes(M, N, K),
@@ -282,6 +316,7 @@ def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, 
 MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
+@_on_its_device
 def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None, workspace=None,
                   stream=None):
     """The orthogonalised direction of an update G [rows, cols] (bf16 or fp32): X =
@@ -293,7 +328,7 @@ def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None
     pg, ldg = _hkg._matrix(G, "G")
     rows, cols = G.shape
     a, b, c = coefficients
-    st = _handle(stream, G)
+    st = _handle(stream, G, out, workspace)
     out, po, ldo = _output(out, (rows, cols), torch.bfloat16, "out", G, stream)
     need = _check(_lib().hkg_orthogonalize_workspace_bytes(rows, cols), "hkg_orthogonalize_workspace_bytes")
     workspace, pws, nws = _workspace(workspace, need, G, stream)
