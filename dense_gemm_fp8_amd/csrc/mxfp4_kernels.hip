@@ -482,8 +482,24 @@ hipError_t launch_mx4_zero(const Mx4GemmParams &p, hipStream_t stream)
     return hipGetLastError();
 }
 
+// A launch's threads have to stay below 2^32, or part of the grid is left out without an
+// error: the columns of a very wide product in turns of 2^27 (2^22 workgroups for up to
+// 16 rows; more rows come with at most 512 workgroups).
+constexpr int kFewCols = 1 << 27;
+
 hipError_t launch_mx4_few_rows(ElemType xt, const Mx4GemmParams &p, hipStream_t stream)
 {
+    if (p.N > kFewCols) {
+        Mx4GemmParams head = p, rest = p;
+        head.N = kFewCols;
+        rest.N -= kFewCols;
+        rest.B += (int64_t)kFewCols * p.kb;
+        rest.SB += (int64_t)kFewCols / kMxStep * ((p.kb + 63) / 64) * kMxStepScales;
+        rest.C += kFewCols;
+        rest.C_f32 += p.C_f32 ? kFewCols : 0;
+        const hipError_t e = launch_mx4_few_rows(xt, head, stream);
+        return e != hipSuccess ? e : launch_mx4_few_rows(xt, rest, stream);
+    }
     const int mb = p.A && p.M > 16 ? 4 : 1;
     const unsigned blocks = few_blocks(p, mb);
     const bool two = two_steps(blocks, p.K);

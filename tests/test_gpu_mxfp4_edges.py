@@ -38,3 +38,27 @@ def test_gradients_over_nothing_are_zero(M, N, K):
     hkg.linear_mxfp4_backward(torch.zeros((M, N), dtype=torch.bfloat16, device="cuda"), codes(K, wide(N)), one(N),
                               codes(K, wide(M)), one(M), dx, dw)
     assert not dx.any() and not dw.any()
+
+
+def test_linear_with_more_columns_than_one_launch_takes():
+    """N = 2^28 + 200: 2^23 workgroups of 512 threads and more for one row of x.  W repeats
+    2^20 rows of codes; its scales are 2^(g mod 3) for the 128 rows of group g."""
+    N, K, period = (1 << 28) + 200, 32, 1 << 20
+    g = torch.Generator("cuda").manual_seed(3)
+    some = torch.randint(0, 256, (period, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    W = torch.empty((N, K // 2), dtype=torch.uint8, device="cuda")
+    for r in range(0, N, period):
+        W[r:r + period].copy_(some[:N - r])
+    groups = -(-N // 128)
+    exponent = torch.arange(groups, device="cuda") % 3
+    packed = (127 + exponent).to(torch.uint8)[:, None].expand(groups, 512).contiguous().view(-1)
+    x = torch.tensor([[0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0] * 4], device="cuda").to(torch.bfloat16)   # its own MXFP4 form
+    y = torch.full((1, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    hkg.linear_mxfp4(x, W, packed, y=y)
+    one = torch.full((period // 128 * 512,), 127, dtype=torch.uint8, device="cuda")
+    values = hkg.mxfp4_dequantize(some, one, hkg.HKG_MX_OPERAND_B, dtype=torch.float32)
+    want = values.double() @ x[0].double()             # multiples of 1/4 below 2^11: exact in fp32
+    for r in range(0, N, period):
+        n = min(period, N - r)
+        e = exponent[r // 128:-(-(r + n) // 128)].repeat_interleave(128)[:n]
+        assert torch.equal(y[0, r:r + n], (want[:n] * torch.exp2(e.double())).float().to(torch.bfloat16))
