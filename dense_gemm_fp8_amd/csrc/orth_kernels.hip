@@ -441,6 +441,7 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void orth_product_kernel(co
     const int tcols = p.cols_t - row0;
     const __amdgpu_buffer_rsrc_t rt =
         buffer_of(to, units && cols > 0 ? (uint32_t)min(cols, St::kSide) * (uint32_t)(2 * p.ldt) : 0u);
+    lanes_in_step();
 #pragma unroll 4
     for (int k = 0; k < St::kSide * St::kUnits / 64; ++k) {
         const int at = 64 * k + lane, u = at % St::kUnits, c = at / St::kUnits;   // rows 8 u .. of column c

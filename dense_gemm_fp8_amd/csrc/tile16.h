@@ -67,6 +67,15 @@ __device__ __forceinline__ void wait_loads()
 }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// Between LDS accesses of a wave's own lanes: the hardware keeps them in order, and this
+// keeps the compiler from moving one lane's read over another lane's write.  No
+// instruction of its own.
+__device__ __forceinline__ void lanes_in_step()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Empty asm statements that keep a value where it is formed: `hold_v` stops the
 // compiler from folding a panel offset into one precomputed address per read,
@@ -539,6 +548,7 @@ struct StageOut {
     {
         if (!units)
             return;
+        lanes_in_step();
 #pragma unroll
         for (int k = 0; k < 16 * St::kUnits / 64; ++k) {
             const int at = 64 * k + lane, row = r0 + at / St::kUnits, u = at % St::kUnits;
@@ -550,6 +560,7 @@ struct StageOut {
     {
         if (units)
             return;
+        lanes_in_step();
         for (int row = 0; row < rows; ++row)
             for (int c = lane; c < min(cols, St::kSide); c += 64)
                 to[row * ld + c] = st.base[St::place(row, c >> 3) + (c & 7)];
