@@ -21,8 +21,6 @@ the wrong kind); nothing has run then.
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 
 import dense_gemm_fp8_amd as _hkg
 
@@ -128,20 +126,26 @@ def _dense(t, name):
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else _hkg._dev_ptr(t, name)
 
 
-def _on_its_device(f):
-    """f with the GPU of its first tensor current, which the launches need: the
-    handle of a device's default stream is 0, and stands for the current device's."""
-    first = next(iter(inspect.signature(f).parameters))
+class _Elsewhere:
+    """The library with GPU `dev` current for each call."""
 
-    @functools.wraps(f)
-    def call(*args, **kw):
-        import torch
-        t = args[0] if args else kw.get(first)
-        if not getattr(t, "is_cuda", False) or t.get_device() == torch.cuda.current_device():
-            return f(*args, **kw)
-        with torch.cuda.device(t.get_device()):
-            return f(*args, **kw)
-    return call
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __getattr__(self, name):
+        def call(*args):
+            import torch
+            with torch.cuda.device(self.dev):
+                return getattr(_lib(), name)(*args)
+        return call
+
+
+def _on(t):
+    """The library for launches on t's GPU, which has to be current: the handle of a
+    device's default stream is 0, and stands for the current device's."""
+    import torch
+    dev = t.get_device()
+    return _lib() if dev == torch.cuda.current_device() else _Elsewhere(dev)
 
 
 def _handle(stream, t, *others) -> int:
@@ -194,7 +198,6 @@ def _workspace(t, need, like, stream):
     return t, _hkg._dev_ptr(t, "workspace"), t.numel() * t.element_size()
 
 
-@_on_its_device
 def mxfp4_quantize(x, operand, stream=None):
     """MXFP4 form of x [rows, K] (bf16 or fp32, rows contiguous) along K ->
     (codes [rows, Kp / 2], packed scales for `operand`)."""
@@ -205,12 +208,11 @@ def mxfp4_quantize(x, operand, stream=None):
     st = _handle(stream, x)
     codes = _empty((rows, _pad32(K) >> 1), torch.uint8, x, stream)
     packed = _bytes(_scale_bytes(rows, K), x, stream)
-    _check(_lib().hkg_mxfp4_quantize(operand, rows, K, px, xt, ld, codes.data_ptr(), packed.data_ptr(),
+    _check(_on(x).hkg_mxfp4_quantize(operand, rows, K, px, xt, ld, codes.data_ptr(), packed.data_ptr(),
                                      st), "hkg_mxfp4_quantize")
     return codes, packed
 
 
-@_on_its_device
 def mxfp4_quantize_both(x, operand, operand_t, stream=None):
     """mxfp4_quantize(x) and, from the same pass over x, the MXFP4 form of x^T
     -> (codes, packed, codes_t [K, Rp / 2], packed_t)."""
@@ -223,13 +225,12 @@ def mxfp4_quantize_both(x, operand, operand_t, stream=None):
     codes_t = _empty((K, _pad32(rows) >> 1), torch.uint8, x, stream)
     packed = _bytes(_scale_bytes(rows, K), x, stream)
     packed_t = _bytes(_scale_bytes(K, rows), x, stream)
-    _check(_lib().hkg_mxfp4_quantize_both(operand, operand_t, rows, K, px, xt, ld, codes.data_ptr(),
+    _check(_on(x).hkg_mxfp4_quantize_both(operand, operand_t, rows, K, px, xt, ld, codes.data_ptr(),
                                           packed.data_ptr(), codes_t.data_ptr(), packed_t.data_ptr(),
                                           st), "hkg_mxfp4_quantize_both")
     return codes, packed, codes_t, packed_t
 
 
-@_on_its_device
 def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     """The values of an MXFP4 matrix, [rows, Kp] in bf16 (default) or fp32."""
     import torch
@@ -242,12 +243,11 @@ def mxfp4_dequantize(codes, packed, operand, out=None, dtype=None, stream=None):
     st = _handle(stream, codes, packed, out)
     dtype = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
     out, po, ld = _output(out, (rows, K), dtype, "out", codes, stream)
-    _check(_lib().hkg_mxfp4_dequantize(operand, rows, K, pc, pp, po, _elem_type(out, "out"), ld,
-                                       st), "hkg_mxfp4_dequantize")
+    _check(_on(codes).hkg_mxfp4_dequantize(operand, rows, K, pc, pp, po, _elem_type(out, "out"), ld,
+                                            st), "hkg_mxfp4_dequantize")
     return out
 
 
-@_on_its_device
 def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
     """C[M,N] (bf16) = A[M,K] · B[N,K]ᵀ of two MXFP4 matrices; returns C."""
     import torch
@@ -265,11 +265,10 @@ def gemm_mxfp4(A, B, SA_packed, SB_packed, C=None, C_f32=None, stream=None):
         C_f32, pf, ldf = _output(C_f32, (M, N), torch.float32, "C_f32", A, stream)
         if ldf != ldc:
             raise ValueError("C and C_f32 must have the same row pitch")
-    _check(_lib().hkg_gemm_mxfp4(M, N, K, pa, pb, sa, sb, pc, pf, ldc, st), "hkg_gemm_mxfp4")
+    _check(_on(A).hkg_gemm_mxfp4(M, N, K, pa, pb, sa, sb, pc, pf, ldc, st), "hkg_gemm_mxfp4")
     return C
 
 
-@_on_its_device
 def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     """y[M,N] (bf16) = Q(x)[M,K] · W[N,K]ᵀ with x quantised to MXFP4 on the way
     (x bf16 or fp32; W, SW_packed an MXFP4 matrix packed for operand B).
@@ -284,12 +283,11 @@ def linear_mxfp4(x, W, SW_packed, y=None, workspace=None, stream=None):
     y, py, ldy = _output(y, (M, N), torch.bfloat16, "y", x, stream)
     need = _check(_lib().hkg_linear_mxfp4_workspace_bytes(M, N, K), "hkg_linear_mxfp4_workspace_bytes")
     workspace, pws, nws = _workspace(workspace, need, x, stream)
-    _check(_lib().hkg_linear_mxfp4(M, N, K, px, xt, ldx, pw, ps, py, ldy, pws, nws, st),
+    _check(_on(x).hkg_linear_mxfp4(M, N, K, px, xt, ldx, pw, ps, py, ldy, pws, nws, st),
            "hkg_linear_mxfp4")
     return y
 
 
-@_on_its_device
 def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, workspace=None,
                           stream=None):
     """Gradients of y = Q(x) Wᵀ, rounding passed straight through: (dx [M,K], dw
@@ -308,15 +306,14 @@ def linear_mxfp4_backward(dy, Wt, SWt_packed, Xt, SXt_packed, dx=None, dw=None, 
     need = _check(_lib().hkg_linear_mxfp4_backward_workspace_bytes(M, N, K),
                   "hkg_linear_mxfp4_backward_workspace_bytes")
     workspace, pws, nws = _workspace(workspace, need, dy, stream)
-    _check(_lib().hkg_linear_mxfp4_backward(M, N, K, pdy, t, lddy, pw, psw, px, psx, pdx, lddx, pdw,
-                                            lddw, pws, nws, st), "hkg_linear_mxfp4_backward")
+    _check(_on(dy).hkg_linear_mxfp4_backward(M, N, K, pdy, t, lddy, pw, psw, px, psx, pdx, lddx, pdw,
+                                             lddw, pws, nws, st), "hkg_linear_mxfp4_backward")
     return dx, dw
 
 
 MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
-@_on_its_device
 def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None, workspace=None,
                   stream=None):
     """The orthogonalised direction of an update G [rows, cols] (bf16 or fp32): X =
@@ -332,6 +329,6 @@ def orthogonalize(G, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None
     out, po, ldo = _output(out, (rows, cols), torch.bfloat16, "out", G, stream)
     need = _check(_lib().hkg_orthogonalize_workspace_bytes(rows, cols), "hkg_orthogonalize_workspace_bytes")
     workspace, pws, nws = _workspace(workspace, need, G, stream)
-    _check(_lib().hkg_orthogonalize(rows, cols, pg, t, ldg, steps, a, b, c, eps, po, ldo, pws, nws, st),
+    _check(_on(G).hkg_orthogonalize(rows, cols, pg, t, ldg, steps, a, b, c, eps, po, ldo, pws, nws, st),
            "hkg_orthogonalize")
     return out
