@@ -326,6 +326,9 @@ int hkg_linear_mxfp4_backward(int64_t M, int64_t N, int64_t K, const void *dy, i
     const bool want_x = dx && M > 0 && K > 0, want_w = dw && N > 0 && K > 0;
     if (!want_x && !want_w)
         return HKG_OK;
+    // the pitch of a gradient that is not asked for means nothing
+    lddx = want_x ? lddx : K;
+    lddw = want_w ? lddw : K;
     int rc = want_x ? check_product(M, K, N, Wt, SWt, dx, &lddx) : HKG_OK;
     if (rc == HKG_OK && want_w)
         rc = check_product(N, K, M, Xt, SXt, dw, &lddw);

@@ -41,7 +41,7 @@ inline int check_matrix(const void *p, int64_t rows, int64_t cols, int64_t elem,
         return HKG_ERR_OPTS;
     if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elem))
         return HKG_ERR_ALIGN;
-    if (rows >= (int64_t(1) << 31) || *ld >= (int64_t(1) << 31))
+    if (rows >= (int64_t(1) << 31) || *ld >= (int64_t(1) << 31) || rows * *ld >= (int64_t(1) << 60))
         return HKG_ERR_SIZE;
     return HKG_OK;
 }
