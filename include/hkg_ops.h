@@ -68,8 +68,10 @@ int hkg_mxfp4_quantize_both(int32_t operand, int32_t operand_t, int64_t rows, in
 
 /*
  * The values an MXFP4 matrix stands for: values [rows][Kp] in bf16 or fp32
- * (v_type), rows ldv elements apart (0 = Kp; ldv >= Kp).  Exact in either type,
- * a block with scale 0xFF gives NaN.
+ * (v_type), rows ldv elements apart (0 = Kp; ldv >= Kp).  Exact in either type
+ * for scales up to 2^125 (code 252, the largest that the quantiser gives); with
+ * codes 253 and 254 magnitudes from 2^128 on are infinity.  A block with scale
+ * 0xFF gives NaN.
  */
 int hkg_mxfp4_dequantize(int32_t operand, int64_t rows, int64_t K, const void *codes,
                          const void *packed, void *values, int32_t v_type, int64_t ldv,
