@@ -44,11 +44,12 @@ OPS_EXPORTS = (
 
 _ready = None
 _raw_stream = None       # device index -> handle of torch's current stream there
+_several = True          # whether there is more than one GPU that a tensor can be on
 
 
 def _lib() -> ctypes.CDLL:
     """libhkg with the argument types of hkg_ops.h set."""
-    global _ready, _raw_stream
+    global _ready, _raw_stream, _several
     if _ready is None:
         lib = _hkg.load()
         i64, i32, p, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
@@ -75,6 +76,7 @@ def _lib() -> ctypes.CDLL:
         # part of a small call's time on the host
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _several = torch.cuda.device_count() > 1
         _ready = lib
     return _ready
 
@@ -143,24 +145,26 @@ class _Elsewhere:
 def _on(t):
     """The library for launches on t's GPU, which has to be current: the handle of a
     device's default stream is 0, and stands for the current device's."""
+    lib = _lib()
+    if not _several:      # the comparisons are a tenth of a small call's time on the host
+        return lib
     import torch
     dev = t.get_device()
-    return _lib() if dev == torch.cuda.current_device() else _Elsewhere(dev)
+    return lib if dev == torch.cuda.current_device() else _Elsewhere(dev)
 
 
 def _handle(stream, t, *others) -> int:
     """Handle of the stream a call runs on: `stream`, or torch's current one on t's
     device; `others`: the call's other tensors, or None."""
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one GPU")
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError("stream must belong to the tensors' GPU")
-        return int(stream.cuda_stream)
     _lib()
-    return _raw_stream(dev)
+    dev = t.get_device()
+    if _several:
+        for o in others:
+            if o is not None and o.get_device() != dev:
+                raise ValueError("all tensors of a call must be on one GPU")
+        if stream is not None and stream.device.index != dev:
+            raise ValueError("stream must belong to the tensors' GPU")
+    return int(stream.cuda_stream) if stream is not None else _raw_stream(dev)
 
 
 def _empty(shape, dtype, like, stream):

@@ -55,6 +55,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(ops, "_lib", lambda: Lib())
     monkeypatch.setattr(ops, "_raw_stream", lambda d: 0)        # every device's default stream
+    monkeypatch.setattr(ops, "_several", True)
     return seen
 
 
