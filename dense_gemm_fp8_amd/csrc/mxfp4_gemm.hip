@@ -1,9 +1,10 @@
 // mxfp4_gemm.hip -- the tiled MXFP4 product for gfx950 (tile16.h's loop with a
 // bf16 epilogue).  Bound by the matrix cores at the clock the power cap leaves
-// them: 16384 x 14336 x 4096 takes 442 us, 4350 TFLOPS at 1.95 GHz; a K step's 128
-// instructions take 2445 cycles back to back and 2630 to 2830 in the loop, and about a
-// fifth of a tile's time is its first loads and its epilogue; 16384^3 reaches 4930
-// TFLOPS.
+// them: 16384 x 14336 x 4096 takes 442 to 472 us by the card, 4350 TFLOPS at 1.95 GHz on
+// the best; a K step's 128 instructions take 2445 cycles back to back and 2630 to 2830 in
+// the loop, and about a fifth of a tile's time is its first loads and its epilogue;
+// 16384^3 reaches 4930 TFLOPS.  The fp32 copy leaves as single elements, which doubles
+// the time (2048 x 4096 x 4096 25 and 49 us, 16384 x 14336 x 4096 456 and 940).
 // 256-tiles read 2 x 128 bytes of operands per 2 x 256 x 256 x 256 operations; a
 // 128-tile twice that, but four times as many of them fill a small grid: 1111 x
 // 2777 x 1184 8.8 us.

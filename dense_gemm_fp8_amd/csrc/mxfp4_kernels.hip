@@ -18,8 +18,10 @@ namespace {
 // wave reads 4 rows of 256 or 512 bytes at once and two DPP steps give a
 // block's largest magnitude.  Along rows: the tile is staged in LDS, a wave
 // takes 32 of its rows and a lane 2 columns, one after the other.  Bound by its
-// bytes: both forms of 14336 x 4096 fp32 (235 MB read, 62 written) in 68 us, 4.4 TB/s,
-// of 8192 x 14336 bf16 (235 and 125) in 84 us, 4.3 TB/s; a 2 GiB copy reaches 4.9.
+// bytes: both forms of 14336 x 4096 fp32 (235 MB read, 62 written) in 60 us, 5.0 TB/s,
+// of 8192 x 14336 bf16 (235 and 125) in 88 us, 4.1 TB/s, with buffers that change from
+// call to call; a 2 GiB copy reaches 4.9.  On the same buffers again, part of which the
+// last-level cache holds, 53 and 84 us.
 constexpr int kQTile = 128;
 
 template <int kElem, bool kBoth>
@@ -114,7 +116,9 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const QuantParams p)
 
 // ---- the values of an MXFP4 matrix ------------------------------------------
 // A lane turns one word of codes (8 elements) into 16 or 32 bytes.  Bound by its
-// bytes: 14336 x 4096 to bf16 (31 MB read, 117 written) in 31 us, 4.8 TB/s.
+// bytes: 14336 x 4096 to bf16 (31 MB read, 117 written) in 37 us, 4.0 TB/s, to fp32 (31
+// and 235) in 63 us, 4.2 TB/s, with buffers that change from call to call; 24 and 51 us
+// on the same ones again, which the last-level cache holds or nearly holds.
 template <int kElem>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams p)
 {
@@ -182,7 +186,9 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const DequantParams
 // the waves' sums are joined in LDS at the end, in a fixed order.  The detour through
 // LDS is what makes the loads whole lines: a lane of a fragment holds 16 bytes of a row
 // of its own, and loaded straight into registers every lane is a request of its own
-// (16 x 8192 x 8192: 15.4 us so, x among them, against 11.4 through LDS).
+// (16 x 8192 x 8192: 15.4 us so, x among them, against 11.4 through LDS).  x with rows that
+// are not 16-byte aligned, or K not a multiple of 32, does go straight to registers, element
+// by element: 1 x 14336 x 4096 18.5 us against 10.5, 16 x 8192 x 8192 47.6 against 11.8.
 // B is the matrix instruction's first operand: fragments 2 j and 2 j + 1 of a packed
 // group then give a lane 8 consecutive columns of one row of C.  kXt: -1 A is codes, 0
 // / 1 x is bf16 / fp32 and each lane quantises the one block that its fragment holds (16

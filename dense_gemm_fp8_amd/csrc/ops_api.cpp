@@ -95,7 +95,10 @@ hkg::Mx4GemmParams product(int64_t M, int64_t N, int64_t K, const void *A, const
 // tiles, which read each operand fewer times.  Measured at 512 blocks: 256 x 4096 x 4096
 // 9.3 us against 10.7 on 128-tiles, 512 x 2048 x 2048 6.3 against 7.2, 256 x 4096 x 14336
 // 24.4 against 35.8; at 896 and 1024: 128 x 14336 x 4096 17.6 against 13.4, 256 x 8192 x
-// 8192 34.5 against 23.2.
+// 8192 34.5 against 23.2.  Up to 128 tiles of 256 (one round of 512 at two a compute unit)
+// 128-tiles: 2048 x 4096 22.9 us against 27.3 at K = 4096 and 65 against 72 at 14336, 2816 x
+// 2816 (121) 22.3 against 26.8; above, 256-tiles: 2048 x 4352 (136) 27.0 against 31.4 and 72
+// against 93.  At K = 512 128-tiles are a tenth faster there, 10.1 against 11.3.
 int product_tile(const hkg::Mx4GemmParams &p)   // 0: the kernel for few rows
 {
     if (ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
@@ -151,8 +154,11 @@ hipError_t run_products(const hkg::Mx4GemmParams &p, const hkg::Mx4GemmParams &p
 }
 
 // Whether the linear layer quantises x inside the product: up to 16 rows, whose part of
-// the work each workgroup then repeats, while that costs less than a launch of its own
-// (16 x 4096 x 14336: 14.1 us against 8.1 + 4; 16 x 8192 x 8192: 11.3 against 9.3 + 4).
+// the work each workgroup then repeats, while that costs less than a launch of its own.
+// In replayed graphs, one launch against two: 1 and 16 x 4096 x 4096 5.0 and 5.7 us against
+// 6.8 and 7.2, x 14336 x 4096 7.7 and 9.7 against 10.0 and 10.6; even at K = 8192 (x 4096 7.7
+// and 8.9 against 8.1 and 8.7); at K = 14336 two are better for one row as for
+// sixteen (x 4096 11.8 and 14.4 against 10.6 and 11.5).
 bool fused_linear(int64_t M, int64_t K) { return M <= 16 && K <= 10240; }
 
 }  // namespace

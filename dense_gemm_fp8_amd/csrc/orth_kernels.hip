@@ -128,8 +128,8 @@ __device__ __forceinline__ f16x8_t low_part(const float (&f)[8])
 // ---- X = G / (|G| + eps), its scaled fp16 form and that of its transpose -----
 // A 64 x 64 tile a workgroup: rows x ps (straight) and cols x pt (transposed), and the
 // fp32 state, zeros past the matrix.  out: with no steps at all, the bf16 result
-// itself.  Bound by its bytes: 14336 x 4096 bf16 reads 117 and writes 470 MB in 117 us,
-// 5.0 TB/s.
+// itself.  Bound by its bytes: 14336 x 4096 bf16 reads 117 and writes 470 MB in 105 to
+// 118 us, 5.0 to 5.6 TB/s.
 template <int kElem>
 __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, const double *partial, int parts,
                                                            float eps, const OrthState state, _Float16 *straight, int ps,
@@ -228,11 +228,12 @@ __global__ __launch_bounds__(256) void orth_convert_kernel(const OrthInput p, co
 
 // ---- a product of a step -----------------------------------------------------
 // Bound by the matrix cores at the clock the power cap leaves, and the update by its
-// state besides: 4096 x 14336 takes 514 us (423 in whole rounds of 256-tiles, 91 in the
-// last one of 128-tiles), of which 235 MB of state read and written take 130, since the
-// tiles of a round end together; the last update, which writes none, 484.  The triangle
-// of a 4096^2 product takes 66 us over K = 4096 and 202 over K = 14336 (253 192-tiles on
-// 256 compute units).
+// state besides: 4096 x 14336 takes 462 to 514 us by the card (378 to 423 in whole rounds of
+// 256-tiles, the cores busy 54 % of the launch, the rest in a last round of 128-tiles), of
+// which 235 MB of state read and written take 80 to 130, since the tiles of a round end
+// together; the last update, which writes none, 412 to 484.  The triangle of a 4096^2
+// product takes 66 us over K = 4096 and 202 to 212 over K = 14336 (253 192-tiles on 256
+// compute units, the cores busy 64 %).
 // Results leave as rows (straight) and / or as columns (transposed), both through a
 // staged quarter of the tile (tile16.h): a symmetric product's D is loaded into it and
 // each lane replaces D's units by its results; whole runs of rows or of columns leave.
