@@ -152,7 +152,7 @@ def gpu_identity() -> dict:
     try:
         import amdsmi
         amdsmi.amdsmi_init()
-        h = amdsmi.amdsmi_get_processor_handles()[0]
+        h = smi_handle(amdsmi)
         out["gpu_serial"] = amdsmi.amdsmi_get_gpu_asic_info(h).get("asic_serial")
         cap = amdsmi.amdsmi_get_power_cap_info(h).get("power_cap")
         out["power_cap_w"] = round(cap / 1e6) if isinstance(cap, (int, float)) else None
@@ -186,16 +186,26 @@ def clock_from_trace(rec: np.ndarray, launches: int) -> dict:
             "workgroups_per_launch": int(rec.shape[1])}
 
 
+def smi_handle(amdsmi):
+    """amdsmi's handle of the current GPU, by its PCI address: amdsmi may list
+    other GPUs of the host, in an order of its own."""
+    import torch
+    d = torch.cuda.get_device_properties(torch.cuda.current_device())
+    bdf = "%04x:%02x:%02x." % (d.pci_domain_id, d.pci_bus_id, d.pci_device_id)
+    return next(h for h in amdsmi.amdsmi_get_processor_handles()
+                if amdsmi.amdsmi_get_gpu_device_bdf(h).lower().startswith(bdf))
+
+
 def metrics_reader():
-    """A callable returning GPU 0's gpu_metrics accumulators from amdsmi as
-    (mem_activity_acc, gfx_activity_acc, accumulation_counter,
-    vram_max_bandwidth in GB/s), or None where amdsmi or these fields are
-    unavailable.  The accumulators advance by the activity in percent per
+    """A callable returning the current GPU's gpu_metrics accumulators from amdsmi
+    as (mem_activity_acc, gfx_activity_acc, accumulation_counter,
+    vram_max_bandwidth in GB/s), or None where amdsmi, this GPU among its or
+    these fields are unavailable.  The accumulators advance by the activity in percent per
     tick of accumulation_counter and are refreshed about once a second."""
     try:
         import amdsmi
         amdsmi.amdsmi_init()
-        h = amdsmi.amdsmi_get_processor_handles()[0]
+        h = smi_handle(amdsmi)
         keys = ("mem_activity_acc", "gfx_activity_acc", "accumulation_counter", "vram_max_bandwidth")
 
         def read():
