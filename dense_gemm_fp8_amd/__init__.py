@@ -496,3 +496,7 @@ HKG_ERR_WORKSPACE = -9
 
 from .ops import (gemm_mxfp4, linear_mxfp4, linear_mxfp4_backward,  # noqa: E402,F401
                   mxfp4_dequantize, mxfp4_quantize, mxfp4_quantize_both, orthogonalize)
+
+# ---- 16-bit linear layer with a fused epilogue, dropout (include/hkg_linear.h) -------
+
+from .linear16 import dropout, linear, linear_backward  # noqa: E402,F401

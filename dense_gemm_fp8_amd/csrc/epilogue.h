@@ -1,0 +1,274 @@
+// epilogue.h -- device code of what a product's results pass through on their way
+// out: bias, activation, dropout, residual (linear_gemm.hip, linear_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linear_kernels.h"
+#include "mx4.h"
+
+namespace hkg {
+
+// ---- the 16-bit types -----------------------------------------------------------
+struct TypeBf16 {
+    __device__ __forceinline__ static float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+    __device__ __forceinline__ static float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
+    __device__ __forceinline__ static uint32_t pack2(float a, float b) { return pack2_bf16(a, b); }
+};
+struct TypeF16 {
+    typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+    __device__ __forceinline__ static float low(uint32_t w) { return (float)__builtin_bit_cast(half2, w)[0]; }
+    __device__ __forceinline__ static float high(uint32_t w) { return (float)__builtin_bit_cast(half2, w)[1]; }
+    __device__ __forceinline__ static uint32_t pack2(float a, float b)   // nearest even; beyond 65504 infinity
+    {
+        const half2 v = {(_Float16)a, (_Float16)b};
+        return __builtin_bit_cast(uint32_t, v);
+    }
+};
+
+// Eight consecutive values of a row.  Rows start anywhere that suits their element:
+// the hardware takes 16-byte accesses at any address.
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ u32x4_t load16(const void *p) { return *static_cast<const u32x4_any_t *>(p); }
+__device__ __forceinline__ void store16(void *p, const u32x4_t &v) { *static_cast<u32x4_any_t *>(p) = v; }
+
+// The first n of the eight elements from p (n < 1: none), the rest zeros.
+template <class T>
+__device__ __forceinline__ void load8_16(const void *p, int n, float (&v)[8])
+{
+    u32x4_t w = {0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        w = load16(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n)
+                w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = T::low(w[e]);
+        v[2 * e + 1] = T::high(w[e]);
+    }
+}
+__device__ __forceinline__ void load8_32(const void *p, int n, float (&v)[8])
+{
+    const uint32_t *f = static_cast<const uint32_t *>(p);
+    u32x4_t a = {0u, 0u, 0u, 0u}, b = a;
+    if (n >= 8) {
+        a = load16(f);
+        b = load16(f + 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n)
+                (e < 4 ? a : b)[e & 3] = f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t x = a[e], y = b[e];   // a bit cast of a vector's element reads element 0
+        v[e] = __builtin_bit_cast(float, x);
+        v[4 + e] = __builtin_bit_cast(float, y);
+    }
+}
+template <class T>
+__device__ __forceinline__ void store8_16(void *p, int n, const float (&v)[8])
+{
+    const u32x4_t w = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])};
+    if (n >= 8) {
+        store16(p, w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n)
+                static_cast<uint16_t *>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+__device__ __forceinline__ void store8_32(void *p, int n, const float (&v)[8])
+{
+    float *f = static_cast<float *>(p);
+    if (n >= 8) {
+        u32x4_t a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            a[e] = __builtin_bit_cast(uint32_t, v[e]);
+            b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
+        }
+        store16(f, a);
+        store16(f + 4, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n)
+                f[e] = v[e];
+    }
+}
+__device__ __forceinline__ const char *element_at(const void *p, int64_t at, int bytes)
+{
+    return static_cast<const char *>(p) + at * bytes;
+}
+__device__ __forceinline__ char *element_at(void *p, int64_t at, int bytes)
+{
+    return static_cast<char *>(p) + at * bytes;
+}
+
+// ---- dropout ----------------------------------------------------------------------
+// One call of Philox-4x32-10: a round multiplies two words by constants and mixes the
+// products' halves with the other two words and the key; the key grows by constants.
+// The 20 multiplications of 32 x 32 bits run at a quarter of the usual rate.
+__device__ __forceinline__ u32x4_t philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1)
+{
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        const uint32_t n0 = (uint32_t)(b >> 32) ^ c1 ^ k0, n2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c1 = (uint32_t)b;
+        c3 = (uint32_t)a;
+        c0 = n0;
+        c2 = n2;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4_t{c0, c1, c2, c3};
+}
+
+// Seed and offset of a launch, in scalar registers.
+struct Key {
+    uint32_t k0, k1, o0, o1;
+    __device__ __forceinline__ explicit Key(const DropoutParams &d)
+    {
+        uint64_t seed = d.seed, offset = d.offset;
+        if (d.rng) {
+            seed = d.rng[0];
+            offset = d.rng[1];
+        }
+        k0 = (uint32_t)seed;
+        k1 = (uint32_t)(seed >> 32);
+        o0 = (uint32_t)offset;
+        o1 = (uint32_t)(offset >> 32);
+    }
+    // the eight numbers of columns 8 group .. 8 group + 7 of a row
+    __device__ __forceinline__ u32x4_t numbers(int row, int group) const
+    {
+        return philox((uint32_t)group, (uint32_t)row, o0, o1, k0, k1);
+    }
+};
+// Whether column e of a group is kept.
+__device__ __forceinline__ bool kept(const u32x4_t &n, int e, uint32_t below)
+{
+    return (e & 1 ? n[e >> 1] >> 16 : n[e >> 1] & 0xffffu) >= below;
+}
+__device__ __forceinline__ void drop8(const DropoutParams &d, const u32x4_t &n, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = kept(n, e, d.below) ? v[e] * d.scale : 0.0f;
+}
+
+// ---- activations ------------------------------------------------------------------
+// v_exp_f32 and v_rcp_f32, both within a unit of fp32's last place: a quarter of the
+// usual rate each, where the library's functions take ten times as long.
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp_of(float x) { return __builtin_amdgcn_rcpf(x); }
+constexpr float kLog2e = 1.44269504f;
+constexpr float kTanhC = 2.0f * 0.79788456f * kLog2e;   // 2 sqrt(2 / pi), for powers of two
+constexpr float kTanhA = 0.044715f;
+constexpr float kLargest = 3.4e38f;
+
+// z, with -infinity replaced by a number: 0 times it is then 0.  A NaN stays one.
+__device__ __forceinline__ float above_minus_inf(float z) { return z < -kLargest ? -kLargest : z; }
+
+// 1 / (1 + 2^-u): 2^-u may be infinity, which gives 0.
+__device__ __forceinline__ float sigmoid2(float u) { return rcp_of(1.0f + exp2_of(-u)); }
+
+// g = exp(-z^2 / 2) and Phi(z).  Phi(-|z|) = g k Q(k) with k = 1 / (1 + 0.24 |z|), Q a
+// polynomial fitted for the smallest relative error over |z| < 40 (4.3e-7): no
+// cancellation on the left, where Phi is small.
+struct Normal {
+    float g, phi;
+    __device__ __forceinline__ explicit Normal(float z)
+    {
+        const float a = __builtin_fabsf(z), k = rcp_of(__builtin_fmaf(0.24f, a, 1.0f));
+        g = exp2_of(z * z * (-0.5f * kLog2e));
+        float q = -0.05299046263f;
+        q = __builtin_fmaf(q, k, 0.15278859437f);
+        q = __builtin_fmaf(q, k, -0.0656934455f);
+        q = __builtin_fmaf(q, k, 0.11838012934f);
+        q = __builtin_fmaf(q, k, 0.06340177357f);
+        q = __builtin_fmaf(q, k, 0.09283750504f);
+        q = __builtin_fmaf(q, k, 0.09552230686f);
+        q = __builtin_fmaf(q, k, 0.09575378895f);
+        const float tail = g * (q * k);
+        phi = z < 0.0f ? tail : 1.0f - tail;
+    }
+};
+
+template <int kAct>
+__device__ __forceinline__ float act_of(float z)
+{
+    if constexpr (kAct == kActRelu)
+        return z <= 0.0f ? 0.0f : z;
+    if constexpr (kAct == kActGelu) {
+        const float c = above_minus_inf(z);
+        return c * Normal(c).phi;
+    }
+    if constexpr (kAct == kActGeluTanh) {
+        const float c = above_minus_inf(z);
+        return c * sigmoid2(c * __builtin_fmaf(kTanhC * kTanhA, c * c, kTanhC));
+    }
+    if constexpr (kAct == kActSilu) {
+        const float c = above_minus_inf(z);
+        return c * sigmoid2(c * kLog2e);
+    }
+    return z;
+}
+// Slopes are constant to fp32's last place beyond +-100; z^2 stays finite there.
+template <int kAct>
+__device__ __forceinline__ float slope_of(float z)
+{
+    if constexpr (kAct == kActRelu)
+        return z <= 0.0f ? 0.0f : z > 0.0f ? 1.0f : z;
+    const float c = z < -100.0f ? -100.0f : z > 100.0f ? 100.0f : z;
+    if constexpr (kAct == kActGelu) {
+        const Normal n(c);
+        return __builtin_fmaf(c * 0.39894228f, n.g, n.phi);   // Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+    }
+    if constexpr (kAct == kActGeluTanh) {
+        const float c2 = c * c, s = sigmoid2(c * __builtin_fmaf(kTanhC * kTanhA, c2, kTanhC));
+        const float du = __builtin_fmaf(3.0f * kTanhA * 1.59576912f, c2, 1.59576912f);   // 2 u'
+        return __builtin_fmaf(c * du, s * (1.0f - s), s);
+    }
+    if constexpr (kAct == kActSilu) {
+        const float s = sigmoid2(c * kLog2e);
+        return __builtin_fmaf(c, s * (1.0f - s), s);
+    }
+    return 1.0f;
+}
+// f on eight values with the activation a constant inside: one uniform branch.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F &&f)
+{
+    switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    default: break;
+    }
+}
+__device__ __forceinline__ void act8(int act, float (&v)[8])
+{
+    with_activation(act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = act_of<decltype(a)::value>(v[e]);
+    });
+}
+__device__ __forceinline__ float act1(int act, float v)
+{
+    with_activation(act, [&](auto a) __attribute__((always_inline)) { v = act_of<decltype(a)::value>(v); });
+    return v;
+}
+
+}  // namespace hkg

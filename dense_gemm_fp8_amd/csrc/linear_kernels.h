@@ -1,0 +1,80 @@
+// linear_kernels.h -- launch interface between the entry points of hkg_linear.h
+// (linear_api.cpp) and their gfx950 kernels (linear_kernels.hip).  Internal to
+// libhkg; all argument checks are done by the caller.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hkg {
+
+enum Activation { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+struct DropoutParams {
+    uint32_t below;                // 65536 q: numbers below it drop; 0: no dropout
+    float scale;                   // 1 / (1 - q)
+    uint64_t seed, offset;
+    const uint64_t *rng;           // device {seed, offset} instead, or null
+};
+
+struct DropoutCall {
+    const void *x, *residual;      // residual may be null
+    void *out;
+    int64_t ldx, ldr, ldo;
+    int rows, cols;
+    DropoutParams drop;
+};
+// x_bits, out_bits: 16 or 32; f16: the 16-bit type is fp16, else bf16
+hipError_t launch_dropout(bool f16, int x_bits, int out_bits, const DropoutCall &p, hipStream_t stream);
+
+// y[M][N] = residual + D(act(A B^T + bias)), A [M][K] and B [N][K] of a 16-bit type.
+struct LinearParams {
+    const uint16_t *A, *B;
+    int64_t lda, ldb;
+    int M, N, K;
+    const void *bias, *residual;   // may be null
+    void *y, *z;                   // z may be null
+    int64_t ldr, ldy, ldz;
+    int bias_f32, y_f32;           // else of the 16-bit type
+    int act;
+    DropoutParams drop;
+    int row0, col0;                // place of [0][0] in the whole result, for dropout; col0 % 8 == 0
+};
+// Rows m .. m + rows - 1 and columns n .. n + cols - 1 of a product.
+inline LinearParams linear_part(const LinearParams &p, int64_t m, int64_t rows, int64_t n, int64_t cols)
+{
+    LinearParams q = p;
+    const int64_t e = p.y_f32 ? 4 : 2;
+    q.M = (int)rows;
+    q.N = (int)cols;
+    q.row0 = p.row0 + (int)m;
+    q.col0 = p.col0 + (int)n;
+    q.A = p.A + m * p.lda;
+    q.B = p.B + n * p.ldb;
+    q.bias = p.bias ? static_cast<const char *>(p.bias) + n * (p.bias_f32 ? 4 : 2) : nullptr;
+    q.residual = p.residual ? static_cast<const char *>(p.residual) + (m * p.ldr + n) * e : nullptr;
+    q.y = static_cast<char *>(p.y) + (m * p.ldy + n) * e;
+    q.z = p.z ? static_cast<char *>(p.z) + (m * p.ldz + n) * 2 : nullptr;
+    return q;
+}
+hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream);
+
+// What the gradients' products read, formed in one pass (any output may be null):
+//   dz  [M][Np] and dzt [N][Mp]   dz and its transpose, zeros past N and M
+//   wt  [K][Np], xt [K][Mp]       the transposes of W [N][K] and x [M][K]
+//   sums [ceil(M / 64)][N]        fp32 column sums of 64 rows of dz each
+// Np, Mp: N and M rounded up to 8.
+struct PrepareParams {
+    const void *dy, *z, *x, *W;
+    int64_t lddy, ldz, ldx, ldw;
+    uint16_t *dz, *dzt, *wt, *xt;
+    float *sums;
+    int M, N, K;
+    int dy_f32, act;
+    DropoutParams drop;
+};
+hipError_t launch_linear_prepare(bool f16, const PrepareParams &p, hipStream_t stream);
+// dbias[N] = the sum of `groups` rows of sums
+hipError_t launch_linear_bias_sum(const float *sums, int groups, int N, float *dbias, hipStream_t stream);
+
+}  // namespace hkg

@@ -1,0 +1,398 @@
+// linear_kernels.hip -- gfx950 kernels of the 16-bit linear layer besides its tiles:
+// dropout, the product of few rows, and what the gradients' products read.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "epilogue.h"
+#include "linear_kernels.h"
+#include "tile16.h"
+
+namespace hkg {
+namespace {
+
+// ---- dropout ----------------------------------------------------------------------
+// A workgroup is 2^s lanes of 8 columns wide, 2^s near a row's groups but at most 256,
+// and takes kRows rows a lane; a lane's loads are all sent before the first is used.
+constexpr int kDropRows = 4;
+
+template <class T, int kXBits, int kOutBits>
+__global__ __launch_bounds__(256) void dropout_kernel(const DropoutCall p, int shift)
+{
+    const int wide = 1 << shift, tall = 256 >> shift;
+    const int group = blockIdx.x * wide + (threadIdx.x & (wide - 1)), col = 8 * group, n = p.cols - col;
+    if (n <= 0)
+        return;
+    const Key key(p.drop);
+    for (int64_t top = (int64_t)blockIdx.y * (tall * kDropRows); top < p.rows; top += (int64_t)gridDim.y * (tall * kDropRows)) {
+        const int64_t row0 = top + (threadIdx.x >> shift);
+        float v[kDropRows][8], r[kDropRows][8];
+#pragma unroll
+        for (int i = 0; i < kDropRows; ++i) {
+            const int64_t row = row0 + i * tall;
+            const int m = row < p.rows ? n : 0;
+            const char *const from = element_at(p.x, row * p.ldx + col, kXBits / 8);
+            if constexpr (kXBits == 16)
+                load8_16<T>(from, m, v[i]);
+            else
+                load8_32(from, m, v[i]);
+            if (p.residual) {
+                const char *const add = element_at(p.residual, row * p.ldr + col, kOutBits / 8);
+                if constexpr (kOutBits == 16)
+                    load8_16<T>(add, m, r[i]);
+                else
+                    load8_32(add, m, r[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDropRows; ++i) {
+            const int64_t row = row0 + i * tall;
+            if (row >= p.rows)
+                continue;
+            if (p.drop.below > 0)
+                drop8(p.drop, key.numbers((int)row, group), v[i]);
+            if (p.residual)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[i][e] += r[i][e];
+            char *const to = element_at(p.out, row * p.ldo + col, kOutBits / 8);
+            if constexpr (kOutBits == 16)
+                store8_16<T>(to, n, v[i]);
+            else
+                store8_32(to, n, v[i]);
+        }
+    }
+}
+
+// ---- the product of few rows --------------------------------------------------------
+// What bounds it is reading B once, so each wave streams its own part of K and keeps a
+// run of loads in flight.  One workgroup computes 16 kMb rows x 32 columns; its 8 waves
+// take runs of kS 32-k steps in turn: wait for the run in LDS, take its fragments into
+// registers, send the next run's loads into the same LDS, multiply while they fly; the
+// waves' sums are joined in LDS in a fixed order.  Loads go through LDS so that a wave's
+// 16-byte chunks form whole lines of rows.
+constexpr int kRowWaves = 8;
+
+template <class T>
+__device__ __forceinline__ f32x4_t mma16(const u32x4_t &a, const u32x4_t &b, const f32x4_t &c)
+{
+    if constexpr (std::is_same_v<T, TypeBf16>) {
+        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                      0, 0, 0);
+    }
+}
+
+template <int kMb, int kS>
+struct RowsPlan {
+    static constexpr int kRow = 64 * kS;                    // bytes of a row in a run
+    static constexpr int kChunks = 4 * kS;
+    static constexpr int kB = 32 * kRow, kA = 16 * kMb * kRow;
+    static constexpr int kWave = kA + kB;                   // LDS bytes of one wave
+    static constexpr int kSums = kRowWaves * 64 * 9 * 4;
+    static constexpr int kLds = kRowWaves * kWave > kSums ? kRowWaves * kWave : kSums;
+    // Places of a row's chunks in LDS, permuted so that the 16 rows of a fragment (B's
+    // differ in bits 0, 1 and 3, 4, A's in 0..3) fall into different 16-byte slots of
+    // the 256-byte bank line.
+    __device__ __forceinline__ static int b_chunk(int row, int c)
+    {
+        return kS == 2 ? c ^ (((row >> 1) & 1) | (((row >> 3) & 3) << 1)) : c ^ ((row >> 3) & 3);
+    }
+    __device__ __forceinline__ static int a_chunk(int row, int c)
+    {
+        return kS == 2 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
+    }
+};
+
+template <class T, int kMb, int kS>
+__global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const LinearParams p)
+{
+    using G = RowsPlan<kMb, kS>;
+    __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int x = lane & 15, q = lane >> 4;
+    const int gn = (p.N + 31) / 32;
+    const int n0 = 32 * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
+    const int kb = 2 * p.K, pitch_a = (int)(2 * p.lda), pitch_b = (int)(2 * p.ldb);
+    const int rows = min(16 * kMb, p.M - m0);
+    char *const lb = smem + wave * G::kWave, *const la = lb + G::kB;
+    // buffers over the workgroup's rows: rows past the matrix read zeros
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(reinterpret_cast<const char *>(p.A) + (int64_t)m0 * pitch_a, panel_range(rows, pitch_a, kb));
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(reinterpret_cast<const char *>(p.B) + (int64_t)n0 * pitch_b, panel_range(min(32, p.N - n0), pitch_b, kb));
+    auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, char *to, int voff) __attribute__((always_inline)) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)to, 16, voff, 0, 0, 0);
+    };
+    constexpr int kLoadRows = 64 / G::kChunks;              // rows of a wave-wide load
+    auto send = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < G::kB / 1024; ++d) {
+            const int row = kLoadRows * d + lane / G::kChunks, at = G::kRow * r + 16 * G::b_chunk(row, lane % G::kChunks);
+            to_lds(rb, lb + 1024 * d, at < kb ? row * pitch_b + at : kPastEnd);
+        }
+#pragma unroll
+        for (int d = 0; d < G::kA / 1024; ++d) {
+            const int row = kLoadRows * d + lane / G::kChunks, at = G::kRow * r + 16 * G::a_chunk(row, lane % G::kChunks);
+            if (kLoadRows * d < rows)                       // past them: whatever LDS holds, in rows not stored
+                to_lds(ra, la + 1024 * d, at < kb ? row * pitch_a + at : kPastEnd);
+        }
+    };
+    f32x4_t acc[kMb][2];
+#pragma unroll
+    for (int i = 0; i < kMb; ++i)
+        acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int runs = (kb + G::kRow - 1) / G::kRow;
+    if (wave < runs)
+        send(wave);
+    const int br = (x & 3) + 8 * (x >> 2);
+    for (int r = wave; r < runs; r += kRowWaves) {
+        u32x4_t b[kS][2], a[kS][kMb];
+        wait_loads<0>();
+#pragma unroll
+        for (int u = 0; u < kS; ++u) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                b[u][h] = *reinterpret_cast<const u32x4_t *>(lb + G::kRow * (br + 4 * h) + 16 * G::b_chunk(br + 4 * h, 4 * u + q));
+#pragma unroll
+            for (int i = 0; i < kMb; ++i)
+                a[u][i] = *reinterpret_cast<const u32x4_t *>(la + G::kRow * (16 * i + x) + 16 * G::a_chunk(x, 4 * u + q));
+        }
+        wait_lds();                                         // the fragments are in registers: their LDS is free
+        if (r + kRowWaves < runs)
+            send(r + kRowWaves);
+#pragma unroll
+        for (int u = 0; u < kS; ++u)
+#pragma unroll
+            for (int i = 0; i < kMb; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    acc[i][h] = mma16<T>(b[u][h], a[u][i], acc[i][h]);
+    }
+    const Key key(p.drop);
+    float(*part)[64][9] = reinterpret_cast<float(*)[64][9]>(smem);   // 9: neighbours' rows fall into other banks
+#pragma unroll
+    for (int i = 0; i < kMb; ++i) {
+        // the sums are complete here for every lane: nothing below may move a
+        // matrix instruction under a lane mask
+        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]));
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            part[wave][lane][e] = acc[i][0][e];
+            part[wave][lane][4 + e] = acc[i][1][e];
+        }
+        __syncthreads();
+        // 16 x 32 results, one a thread: lane 16 (c / 8) + r of the fragments holds row r, column c
+        const int r = threadIdx.x >> 5, c = threadIdx.x & 31, row = m0 + 16 * i + r, col = n0 + c;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w)
+            v += part[w][16 * (c >> 3) + r][c & 7];
+        if (row >= p.M || col >= p.N)
+            continue;
+        if (p.bias)
+            v += p.bias_f32 ? static_cast<const float *>(p.bias)[col] : T::low(static_cast<const uint16_t *>(p.bias)[col]);
+        if (p.z)
+            static_cast<uint16_t *>(p.z)[row * p.ldz + col] = (uint16_t)T::pack2(v, 0.f);
+        v = act1(p.act, v);
+        if (p.drop.below > 0)
+            v = kept(key.numbers(p.row0 + row, (p.col0 + col) >> 3), col & 7, p.drop.below) ? v * p.drop.scale : 0.0f;
+        const int64_t at = row * p.ldy + col, from = row * p.ldr + col;
+        if (p.y_f32) {
+            if (p.residual)
+                v += static_cast<const float *>(p.residual)[from];
+            static_cast<float *>(p.y)[at] = v;
+        } else {
+            if (p.residual)
+                v += T::low(static_cast<const uint16_t *>(p.residual)[from]);
+            static_cast<uint16_t *>(p.y)[at] = (uint16_t)T::pack2(v, 0.f);
+        }
+    }
+}
+
+// ---- what the gradients' products read ------------------------------------------------
+// 64 x 64 tiles through LDS: a tile of dz, of W or of x a workgroup.  A lane reads 8
+// elements of a row, and for the transpose gathers 8 of a column from LDS, whose rows
+// are 66 elements long so that the gather's neighbours meet different banks.
+constexpr int kPrep = 64;
+constexpr int kPrepPitch = 66;
+
+template <class T>
+__global__ __launch_bounds__(256) void linear_prepare_kernel(const PrepareParams p, int dz_tiles, int w_tiles)
+{
+    __shared__ uint16_t tile[kPrep * kPrepPitch];
+    __shared__ float part[32][kPrep];
+    int b = blockIdx.x;
+    const int what = b < dz_tiles ? 0 : b < dz_tiles + w_tiles ? 1 : 2;
+    b -= what == 0 ? 0 : what == 1 ? dz_tiles : dz_tiles + w_tiles;
+    const int rows = what == 1 ? p.N : p.M, cols = what == 0 ? p.N : p.K;
+    const int gc = (cols + kPrep - 1) / kPrep, r0 = kPrep * (b / gc), c0 = kPrep * (b % gc);
+    uint16_t *const to = what == 0 ? p.dz : nullptr, *const to_t = what == 0 ? p.dzt : what == 1 ? p.wt : p.xt;
+    const int64_t ld = (cols + 7) & ~7, ld_t = (rows + 7) & ~7;
+    const int g = threadIdx.x & 7, c = c0 + 8 * g;          // the lane's columns
+    const Key key(p.drop);
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kPrep / 32; ++i) {
+        const int rl = (threadIdx.x >> 3) + 32 * i, row = r0 + rl, n = row < rows ? cols - c : 0;
+        float v[8];
+        if (what == 0) {
+            if (p.dy_f32)
+                load8_32(element_at(p.dy, row * p.lddy + c, 4), n, v);
+            else
+                load8_16<T>(element_at(p.dy, row * p.lddy + c, 2), n, v);
+            if (p.act != kActNone) {
+                float z[8];
+                load8_16<T>(element_at(p.z, row * p.ldz + c, 2), n, z);
+                with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = e < n ? v[e] * slope_of<decltype(a)::value>(z[e]) : 0.0f;
+                });
+            }
+            if (p.drop.below > 0)
+                drop8(p.drop, key.numbers(row, c >> 3), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] += v[e];
+        } else {
+            const int64_t at = (int64_t)row * (what == 1 ? p.ldw : p.ldx) + c;
+            load8_16<T>(element_at(what == 1 ? p.W : p.x, at, 2), n, v);
+        }
+        const u32x4_t w = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])};
+        if (to && row < rows && c < cols)
+            store16(to + row * ld + c, w);                  // rows of whole groups: zeros past the last column
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint32_t *>(&tile[rl * kPrepPitch + 8 * g + 2 * e]) = w[e];
+    }
+    if (what == 0 && p.sums) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            part[threadIdx.x >> 3][8 * g + e] = sum[e];
+    }
+    __syncthreads();
+    if (to_t) {
+#pragma unroll
+        for (int i = 0; i < kPrep / 32; ++i) {
+            const int cl = (threadIdx.x >> 3) + 32 * i, col = c0 + cl, row = r0 + 8 * g;
+            u32x4_t w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = tile[(8 * g + 2 * e) * kPrepPitch + cl] | (uint32_t)tile[(8 * g + 2 * e + 1) * kPrepPitch + cl] << 16;
+            if (col < cols && row < rows)
+                store16(to_t + col * ld_t + row, w);        // rows past the matrix are zeros in the tile
+        }
+    }
+    if (what == 0 && p.sums && threadIdx.x < kPrep && c0 + (int)threadIdx.x < cols) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s += part[i][threadIdx.x];
+        p.sums[(int64_t)(r0 / kPrep) * cols + c0 + threadIdx.x] = s;
+    }
+}
+
+__global__ __launch_bounds__(256) void linear_bias_sum_kernel(const float *sums, int groups, int N, float *dbias)
+{
+    __shared__ float part[8][32];
+    const int c = threadIdx.x & 31, w = threadIdx.x >> 5, col = 32 * blockIdx.x + c;
+    float s = 0.f;
+    if (col < N)
+        for (int g = w; g < groups; g += 8)
+            s += sums[(int64_t)g * N + col];
+    part[w][c] = s;
+    __syncthreads();
+    if (w == 0 && col < N) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t += part[i][c];
+        dbias[col] = t;
+    }
+}
+
+template <class T, int kMb, int kS>
+hipError_t few_rows(const LinearParams &p, unsigned blocks, hipStream_t stream)
+{
+    hipLaunchKernelGGL((linear_few_rows_kernel<T, kMb, kS>), dim3(blocks), dim3(64 * kRowWaves), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t few_rows_of(const LinearParams &p, hipStream_t stream)
+{
+    const int mb = p.M > 16 ? 4 : 1;
+    const unsigned blocks = (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
+    if (mb == 1)
+        return few_rows<T, 1, 2>(p, blocks, stream);
+    return few_rows<T, 4, 2>(p, blocks, stream);
+}
+
+template <class T, int kXBits, int kOutBits>
+hipError_t dropout_of(const DropoutCall &p, hipStream_t stream)
+{
+    const int groups = (p.cols + 7) / 8;
+    int shift = 0;
+    while (shift < 8 && (1 << shift) < groups)
+        ++shift;
+    const int64_t tall = (256 >> shift) * kDropRows, high = (p.rows + tall - 1) / tall, wide = (groups + (1 << shift) - 1) >> shift;
+    // at most 2^23 workgroups, so that their threads stay below 2^32; more rows in turns
+    int64_t turn = (int64_t(1) << 23) / wide;               // wide is at most 2^20
+    turn = turn < 65535 ? turn : 65535;
+    const dim3 grid((unsigned)wide, (unsigned)(high < turn ? high : turn));
+    hipLaunchKernelGGL((dropout_kernel<T, kXBits, kOutBits>), grid, dim3(256), 0, stream, p, shift);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dropout(bool f16, int x_bits, int out_bits, const DropoutCall &p, hipStream_t stream)
+{
+    if (x_bits == 32)
+        return dropout_of<TypeBf16, 32, 32>(p, stream);
+    if (f16)
+        return out_bits == 32 ? dropout_of<TypeF16, 16, 32>(p, stream) : dropout_of<TypeF16, 16, 16>(p, stream);
+    return out_bits == 32 ? dropout_of<TypeBf16, 16, 32>(p, stream) : dropout_of<TypeBf16, 16, 16>(p, stream);
+}
+
+// A launch's threads have to stay below 2^32, or part of the grid is left out without an
+// error: turns of at most 2^22 workgroups.
+hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream)
+{
+    constexpr int64_t kMost = int64_t(1) << 22;
+    const int64_t high = p.M > 16 ? ((int64_t)p.M + 63) / 64 : 1;
+    const int64_t turn_m = high < kMost ? p.M : 64 * kMost, turn_n = 32 * (high < kMost ? kMost / high : 1);
+    hipError_t e = hipSuccess;
+    for (int64_t m = 0; m < p.M && e == hipSuccess; m += turn_m)
+        for (int64_t n = 0; n < p.N && e == hipSuccess; n += turn_n) {
+            const LinearParams q = linear_part(p, m, p.M - m < turn_m ? p.M - m : turn_m, n, p.N - n < turn_n ? p.N - n : turn_n);
+            e = f16 ? few_rows_of<TypeF16>(q, stream) : few_rows_of<TypeBf16>(q, stream);
+        }
+    return e;
+}
+
+hipError_t launch_linear_prepare(bool f16, const PrepareParams &p, hipStream_t stream)
+{
+    const auto tiles = [](int64_t r, int64_t c) { return (r + kPrep - 1) / kPrep * ((c + kPrep - 1) / kPrep); };
+    const int64_t dz = p.dz || p.dzt || p.sums ? tiles(p.M, p.N) : 0, w = p.wt ? tiles(p.N, p.K) : 0,
+                  x = p.xt ? tiles(p.M, p.K) : 0;
+    if (dz + w + x == 0)
+        return hipSuccess;
+    if (f16)
+        hipLaunchKernelGGL(linear_prepare_kernel<TypeF16>, dim3((unsigned)(dz + w + x)), dim3(256), 0, stream, p, (int)dz, (int)w);
+    else
+        hipLaunchKernelGGL(linear_prepare_kernel<TypeBf16>, dim3((unsigned)(dz + w + x)), dim3(256), 0, stream, p, (int)dz, (int)w);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_bias_sum(const float *sums, int groups, int N, float *dbias, hipStream_t stream)
+{
+    hipLaunchKernelGGL(linear_bias_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, sums, groups, N, dbias);
+    return hipGetLastError();
+}
+
+}  // namespace hkg
