@@ -15,7 +15,8 @@ SOURCES = [os.path.join(CSRC, "gemm_kernels.hip"), os.path.join(CSRC, "hkg_api.c
            os.path.join(CSRC, "tune.cpp"), os.path.join(CSRC, "mxfp4_kernels.hip"),
            os.path.join(CSRC, "mxfp4_gemm.hip"), os.path.join(CSRC, "ops_api.cpp"),
            os.path.join(CSRC, "orth_kernels.hip"), os.path.join(CSRC, "orth_api.cpp"),
-           os.path.join(CSRC, "linear_kernels.hip"), os.path.join(CSRC, "linear_api.cpp")]
+           os.path.join(CSRC, "linear_kernels.hip"),
+           os.path.join(CSRC, "linear_gemm.hip"), os.path.join(CSRC, "linear_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -53,10 +53,25 @@ int check_operand(const void *p, int64_t rows, int64_t cols, int64_t *ld)
 // Whether out may share its bytes with the input at `in`: the same matrix, element for element.
 bool same_matrix(const void *out, int64_t ldo, const void *in, int64_t ldi) { return out == in && ldo == ldi; }
 
-// The product and its epilogue, on arguments that are checked.
+// The product and its epilogue, on arguments that are checked.  Up to 512 blocks of 64 x
+// 32 results (two for each compute unit) the kernel for few rows, which splits K over a
+// workgroup's waves; above, the launches that the bf16 GEMM makes of this shape.
 hipError_t run_linear(bool f16, const hkg::LinearParams &p, hipStream_t stream)
 {
-    return hkg::launch_linear_few_rows(f16, p, stream);
+    if (p.K == 0 || p.M <= 16 || ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
+        return hkg::launch_linear_few_rows(f16, p, stream);
+    Plan pl;
+    if (plan_gemm(hkg::kBf16, p.M, p.N, p.K, nullptr, &pl) != HKG_OK)
+        return hipErrorInvalidValue;
+    hipError_t e = hipSuccess;
+    int64_t row = 0;
+    for (int i = 0; i < pl.launches && e == hipSuccess; ++i) {
+        const hkg::TileGrid g = {static_cast<int>(tile_edge(pl.sched[i])), static_cast<int>(pl.Gm[i]),
+                                 static_cast<int>(pl.Gn[i]), pl.W[i], pl.C[i]};
+        e = hkg::launch_linear_tiles(f16, g, hkg::linear_part(p, row, pl.rows[i], 0, p.N), stream);
+        row += pl.rows[i];
+    }
+    return e;
 }
 
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }

@@ -57,6 +57,11 @@ inline LinearParams linear_part(const LinearParams &p, int64_t m, int64_t rows, 
     q.z = p.z ? static_cast<char *>(p.z) + (m * p.ldz + n) * 2 : nullptr;
     return q;
 }
+// A grid of Gm x Gn tiles of edge `tile` (256, 192 or 128) and its order (remap.h).
+struct TileGrid {
+    int tile, Gm, Gn, W, C;
+};
+hipError_t launch_linear_tiles(bool f16, const TileGrid &g, const LinearParams &p, hipStream_t stream);   // K > 0
 hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream);
 
 // What the gradients' products read, formed in one pass (any output may be null):

@@ -1,6 +1,6 @@
 // tile16.h -- the tiled product loop of the operators' kernels: C = A B^T for
 // operands whose matrix-instruction fragment is 16 bytes a lane, MXFP4 (32 e2m1
-// elements with a block scale) and fp16 (8 elements).
+// elements with a block scale), fp16 and bf16 (8 elements).
 //
 // One workgroup of 4 waves computes a kT x kT tile (kT = 256, 192 or 128), wave
 // w the quarter (w >> 1, w & 1): kB x kB blocks of 16 x 16, kB = kT / 32.  The K
@@ -48,6 +48,7 @@ constexpr int kLoadBytes = 1024;                 // one wave-wide load to LDS: 8
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 // Slot permutations: A's fragment reads vary row bits 1, 2, 3 within 16 lanes
 // (rows 16 i + x), B's bits 1, 3, 4; two rows share a bank line.
@@ -141,8 +142,9 @@ struct StepScales {
     uint32_t a[2][kB == 8 ? 2 : 1], b[2][kB == 8 ? 2 : 1];
 };
 
+// kScaled: block scales; kMasked: rows may end inside a K step (at whole 16-byte chunks).
 struct F16 {
-    static constexpr bool kScaled = false;
+    static constexpr bool kScaled = false, kMasked = false;
     template <int kI, int kJ, int kB>
     __device__ __forceinline__ static f32x4_t mma(const u32x4_t &b, const u32x4_t &a, const f32x4_t &c,
                                                   const StepScales<kB> &, int)
@@ -151,8 +153,21 @@ struct F16 {
                                                       __builtin_bit_cast(f16x8_t, a), c, 0, 0, 0);
     }
 };
+struct F16Masked : F16 {
+    static constexpr bool kMasked = true;
+};
+struct Bf16Masked {
+    static constexpr bool kScaled = false, kMasked = true;
+    template <int kI, int kJ, int kB>
+    __device__ __forceinline__ static f32x4_t mma(const u32x4_t &b, const u32x4_t &a, const f32x4_t &c,
+                                                  const StepScales<kB> &, int)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b),
+                                                       __builtin_bit_cast(bf16x8_t, a), c, 0, 0, 0);
+    }
+};
 struct F4 {
-    static constexpr bool kScaled = true;
+    static constexpr bool kScaled = true, kMasked = true;
     template <int kI, int kJ, int kB>
     __device__ __forceinline__ static f32x4_t mma(const u32x4_t &b, const u32x4_t &a, const f32x4_t &c,
                                                   const StepScales<kB> &s, int half)
@@ -333,7 +348,7 @@ struct TileLoop {
     __device__ __forceinline__ void run(f32x4_t (&acc)[kB][kB], int nk)
     {
         constexpr int kHi = kB == 8;             // the last scale word
-        constexpr bool kMasked = Mma::kScaled;   // fp16 operands come padded to whole K steps
+        constexpr bool kMasked = Mma::kMasked;
         StepScales<kB> sc = {};
         if constexpr (Mma::kScaled)
             scales(sc, 0, min(kMxStepScales, s_last));   // first: the wait below covers it
