@@ -376,6 +376,12 @@ struct TileLoop {
             for (int i = 0; i < kB; ++i)
                 f.a[0][i] = *reinterpret_cast<const u32x4_t *>(smem + blk_a(i) + ba);
         }
+        // Nothing is on its way from LDS when the loop begins: the compiler, which orders
+        // the reads above as it likes, else waits at the loop's head for every read in
+        // flight, the next half's among them, in all of the steps.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
         // LDS offsets of the wave's first row group in A(t), A(t+1), B(t), B(t+1),
         // B(t+2), and of its fragments' rows from there; K bytes of step t+2
         int pa = w_load, pa1 = pa + kPanel, pb = w_load + kRingB, pb1 = pb + kPanel, pb2 = pb1 + kPanel;
