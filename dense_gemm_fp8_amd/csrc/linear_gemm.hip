@@ -24,6 +24,7 @@ struct F32Stage {
     static constexpr int kLanes = kSide / 8;                           // lanes of a row on the way back
     static constexpr int kTurn = kB == 6 ? 3 : 4;                      // groups of a lane in a turn
     static constexpr int kTurnRows = 64 * kTurn / kLanes, kTurns = kRows / kTurnRows;
+    static constexpr bool kAligned = 64 % kLanes == 0;                 // a lane's groups share their columns
     static_assert(64 * kTurn % kLanes == 0 && kRows % kTurnRows == 0, "whole turns");
     // Where unit u of a row is: permuted so that 16 lanes with one unit of 16 rows, and 16
     // lanes with every other unit of one or two rows, meet different slots of the 256-byte
@@ -35,9 +36,224 @@ struct F32Stage {
     }
 };
 
+// Four accumulators to LDS: from the AGPRs of 256 and 192 tiles without a detour through
+// VGPRs, for which the compiler takes two instructions an element.  The caller sees to it
+// that the matrix instructions are done.
+template <int kB, int kOffset>
+__device__ __forceinline__ void acc_to_lds(int at, const f32x4_t &v)
+{
+    if constexpr (kB >= 6)
+        asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(at), "a"(v), "n"(kOffset) : "memory");
+    else
+        asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(at), "v"(v), "n"(kOffset) : "memory");
+}
+
 // Raw residual values of 8 columns, 16 or 32 bits each.
 struct Raw8 {
     u32x4_t a, b;
+};
+
+// The rows of one matrix that a lane goes through: an address per group, moved on by
+// whole turns.
+template <int kB>
+struct RowPtr {
+    using St = F32Stage<kB>;
+    char *at[St::kAligned ? 1 : St::kTurn];
+    int64_t group, turn;                                     // bytes from group to group (aligned), turn to turn
+    __device__ __forceinline__ void init(const void *base, int64_t ld, int bytes, int row, int col, int lane)
+    {
+        ld *= bytes;
+        turn = St::kTurnRows * ld;
+        group = 64 / St::kLanes * ld;
+#pragma unroll
+        for (int u = 0; u < (St::kAligned ? 1 : St::kTurn); ++u)
+            at[u] = static_cast<char *>(const_cast<void *>(base)) + (row + (64 * u + lane) / St::kLanes) * ld +
+                    (int64_t)(col + 8 * ((64 * u + lane) % St::kLanes)) * bytes;
+    }
+    __device__ __forceinline__ char *get(int u) const { return St::kAligned ? at[0] + u * group : at[u]; }
+    __device__ __forceinline__ void next()
+    {
+#pragma unroll
+        for (int u = 0; u < (St::kAligned ? 1 : St::kTurn); ++u)
+            at[u] += turn;
+    }
+};
+
+// From accumulators to results: the quarter's rows in passes of what LDS holds, a pass in
+// turns of kTurn groups of 8 columns a lane.  kWhole: the quarter lies inside the matrix.
+template <class T, int kB, bool kWhole>
+struct Epilogue {
+    using St = F32Stage<kB>;
+    const LinearParams &p;
+    char *const mine;
+    const int lane, row0, col0;
+    int col[St::kTurn];
+    float bias[St::kTurn][8];
+    RowPtr<kB> y, z, r;
+    Raw8 next[St::kTurn];
+
+    __device__ __forceinline__ int columns(int u) const { return kWhole ? 8 : hold_v(p.N - col[u]); }   // (held: else the
+    // comparisons with it stay in registers for the whole loop)
+
+    __device__ __forceinline__ Epilogue(const LinearParams &params, char *lds, int l, int r0, int c0)
+        : p(params), mine(lds), lane(l), row0(r0), col0(c0)
+    {
+#pragma unroll
+        for (int u = 0; u < St::kTurn; ++u)
+            col[u] = col0 + 8 * ((64 * u + lane) % St::kLanes);
+        y.init(p.y, p.ldy, p.y_f32 ? 4 : 2, row0, col0, lane);
+        if (p.z)
+            z.init(p.z, p.ldz, 2, row0, col0, lane);
+        if (p.residual)
+            r.init(p.residual, p.ldr, p.y_f32 ? 4 : 2, row0, col0, lane);
+        if (p.bias)
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u) {
+                if (St::kAligned && u > 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        bias[u][e] = bias[0][e];
+                } else if (p.bias_f32) {
+                    load8_32(element_at(p.bias, col[u], 4), columns(u), bias[u]);
+                } else {
+                    load8_16<T>(element_at(p.bias, col[u], 2), columns(u), bias[u]);
+                }
+            }
+    }
+    // Row of group u of a turn, from the quarter's first.
+    __device__ __forceinline__ int row_of(int turn, int u) const { return turn * St::kTurnRows + (64 * u + lane) / St::kLanes; }
+    __device__ __forceinline__ bool inside(int turn, int u) const { return kWhole || row0 + row_of(turn, u) < p.M; }
+
+    // The residual's values of a turn, and on to the next.
+    __device__ __forceinline__ void fetch(int turn)
+    {
+        if (!p.residual || turn >= St::kPasses * St::kTurns)
+            return;
+#pragma unroll
+        for (int u = 0; u < St::kTurn; ++u) {
+            const int m = columns(u);
+            const char *const from = r.get(u);
+            Raw8 w = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+            if (inside(turn, u)) {
+                if (m >= 8) {
+                    w.a = load16(from);
+                    if (p.y_f32)
+                        w.b = load16(from + 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 7; ++e)
+                        if (e < m) {
+                            if (p.y_f32)
+                                (e < 4 ? w.a : w.b)[e & 3] = reinterpret_cast<const uint32_t *>(from)[e];
+                            else
+                                w.a[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(from)[e] << (16 * (e & 1));
+                        }
+                }
+            }
+            next[u] = w;
+        }
+        r.next();
+    }
+    // One turn, whose rows start `local` rows into what LDS holds.
+    __device__ __forceinline__ void one(const Key &key, int turn, int local)
+    {
+        float v[St::kTurn][8];
+#pragma unroll
+        for (int u = 0; u < St::kTurn; ++u) {
+            const int rl = local + (64 * u + lane) / St::kLanes, first = (col[u] - col0) >> 2;
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(mine + St::place(rl, first));
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(mine + St::place(rl, first + 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[u][e] = lo[e];
+                v[u][4 + e] = hi[e];
+            }
+        }
+        Raw8 now[St::kTurn];
+#pragma unroll
+        for (int u = 0; u < St::kTurn; ++u)
+            now[u] = next[u];
+        fetch(turn + 1);
+        if (p.bias)
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[u][e] += bias[u][e];
+        if (p.z) {
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+                if (inside(turn, u))
+                    store8_16<T>(z.get(u), columns(u), v[u]);
+            z.next();
+        }
+        with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[u][e] = act_of<decltype(a)::value>(v[u][e]);
+        });
+        if (p.drop.below > 0)
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+                drop8(p.drop, key.numbers(p.row0 + row0 + row_of(turn, u), (p.col0 + col[u]) >> 3), v[u]);
+        if (p.y_f32) {
+            if (p.residual)
+#pragma unroll
+                for (int u = 0; u < St::kTurn; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a = now[u].a[e], b = now[u].b[e];
+                        v[u][e] += __builtin_bit_cast(float, a);
+                        v[u][4 + e] += __builtin_bit_cast(float, b);
+                    }
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+                if (inside(turn, u))
+                    store8_32(y.get(u), columns(u), v[u]);
+        } else {
+            if (p.residual)
+#pragma unroll
+                for (int u = 0; u < St::kTurn; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[u][2 * e] += T::low(now[u].a[e]);
+                        v[u][2 * e + 1] += T::high(now[u].a[e]);
+                    }
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u)
+                if (inside(turn, u))
+                    store8_16<T>(y.get(u), columns(u), v[u]);
+        }
+        y.next();
+    }
+    __device__ __forceinline__ void run(f32x4_t (&acc)[kB][kB])
+    {
+        const Key key(p.drop);
+        const int x = lane & 15, q = lane >> 4;
+        int to[kB];                                          // LDS address of the lane's unit of column block j
+#pragma unroll
+        for (int j = 0; j < kB; ++j)                         // columns 32 (j / 2) + 8 q + 4 (j % 2) ..
+            to[j] = (int)(uintptr_t)(__attribute__((address_space(3))) char *)mine +
+                    St::place(x, 8 * (j >> 1) + 2 * q + (j & 1));
+        fetch(0);
+        for (int pass = 0; pass < St::kPasses; ++pass) {
+            slots<St::kPasses>([&](auto which) __attribute__((always_inline)) {
+                if (pass == decltype(which)::value)
+                    slots<St::kBlocks>([&](auto b) __attribute__((always_inline)) {
+                        constexpr int k = decltype(b)::value;
+#pragma unroll
+                        for (int j = 0; j < kB; ++j)
+                            acc_to_lds<kB, 16 * k * St::kUnits * 16>(to[j], acc[decltype(which)::value * St::kBlocks + k][j]);
+                    });
+            });
+            lanes_in_step();
+            for (int turn = 0; turn < St::kTurns; ++turn)
+                one(key, pass * St::kTurns + turn, turn * St::kTurnRows);
+            lanes_in_step();                                 // the next pass overwrites these rows
+        }
+    }
 };
 
 template <class T, class Mma, int kT>
@@ -45,8 +261,7 @@ __device__ __forceinline__ void linear_tile(const TileOperands &o, const LinearP
 {
     using Loop = TileLoop<Mma, kT>;
     constexpr int kB = Loop::kB;
-    using St = F32Stage<kB>;
-    static_assert(4 * St::kBytes <= Loop::kLds, "the stage fits");
+    static_assert(4 * F32Stage<kB>::kBytes <= Loop::kLds, "the stage fits");
     int tm, tn;
     remap_tile(block, o.Gm, o.Gn, o.W, o.C, tm, tn);
     f32x4_t acc[kB][kB];
@@ -59,132 +274,14 @@ __device__ __forceinline__ void linear_tile(const TileOperands &o, const LinearP
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
     settle(acc);
-    const int lane = loop.lane, x = lane & 15, q = lane >> 4;
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");       // the last matrix instructions' results are there
     const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
-    const int ye = p.y_f32 ? 4 : 2;
-    // group u of a turn: 8 columns of one row
-    int lrow[St::kTurn], col[St::kTurn], n[St::kTurn];
-    float bias[St::kTurn][8];
-#pragma unroll
-    for (int u = 0; u < St::kTurn; ++u) {
-        lrow[u] = (64 * u + lane) / St::kLanes;
-        col[u] = col0 + 8 * ((64 * u + lane) % St::kLanes);
-        n[u] = p.N - col[u];
-        if (!p.bias) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                bias[u][e] = 0.0f;
-        } else if (p.bias_f32) {
-            load8_32(element_at(p.bias, col[u], 4), n[u], bias[u]);
-        } else {
-            load8_16<T>(element_at(p.bias, col[u], 2), n[u], bias[u]);
-        }
-    }
-    const Key key(p.drop);
-    char *const mine = smem + loop.wave * St::kBytes;
+    char *const mine = smem + loop.wave * F32Stage<kB>::kBytes;
     barrier();   // every wave has read its last fragments
-#pragma unroll
-    for (int pass = 0; pass < St::kPasses; ++pass) {
-        const int top = row0 + pass * St::kRows;
-#pragma unroll
-        for (int b = 0; b < St::kBlocks; ++b) {
-            const int i = pass * St::kBlocks + b;
-            settle_row(acc, i);
-#pragma unroll
-            for (int j = 0; j < kB; ++j)   // columns 32 (j / 2) + 8 q + 4 (j % 2) ..
-                *reinterpret_cast<f32x4_t *>(mine + St::place(16 * b + x, 8 * (j >> 1) + 2 * q + (j & 1))) = acc[i][j];
-        }
-        lanes_in_step();
-        auto fetch = [&](int turn, int u) __attribute__((always_inline)) {
-            Raw8 r = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-            const int row = top + turn * St::kTurnRows + lrow[u];
-            const int m = hold_v(n[u]);   // else the comparisons below are kept in registers for the whole loop
-            if (!p.residual || turn >= St::kTurns || row >= p.M || m <= 0)
-                return r;
-            const char *const from = element_at(p.residual, row * p.ldr + col[u], ye);
-            if (m >= 8) {
-                r.a = load16(from);
-                if (p.y_f32)
-                    r.b = load16(from + 16);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    if (e < m) {
-                        if (p.y_f32)
-                            (e < 4 ? r.a : r.b)[e & 3] = reinterpret_cast<const uint32_t *>(from)[e];
-                        else
-                            r.a[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(from)[e] << (16 * (e & 1));
-                    }
-            }
-            return r;
-        };
-        Raw8 next[St::kTurn];
-#pragma unroll
-        for (int u = 0; u < St::kTurn; ++u)
-            next[u] = fetch(0, u);
-        for (int turn = 0; turn < St::kTurns; ++turn) {
-            float v[St::kTurn][8];
-            Raw8 now[St::kTurn];
-#pragma unroll
-            for (int u = 0; u < St::kTurn; ++u) {
-                const int r = turn * St::kTurnRows + lrow[u], first = (col[u] - col0) >> 2;
-                const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(mine + St::place(r, first));
-                const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(mine + St::place(r, first + 1));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[u][e] = lo[e] + bias[u][e];
-                    v[u][4 + e] = hi[e] + bias[u][4 + e];
-                }
-                now[u] = next[u];
-            }
-#pragma unroll
-            for (int u = 0; u < St::kTurn; ++u)
-                next[u] = fetch(turn + 1, u);
-            if (p.z)
-#pragma unroll
-                for (int u = 0; u < St::kTurn; ++u) {
-                    const int row = top + turn * St::kTurnRows + lrow[u];
-                    if (row < p.M)
-                        store8_16<T>(element_at(p.z, row * p.ldz + col[u], 2), hold_v(n[u]), v[u]);
-                }
-            with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
-#pragma unroll
-                for (int u = 0; u < St::kTurn; ++u)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[u][e] = act_of<decltype(a)::value>(v[u][e]);
-            });
-            if (p.drop.below > 0)
-#pragma unroll
-                for (int u = 0; u < St::kTurn; ++u)
-                    drop8(p.drop, key.numbers(p.row0 + top + turn * St::kTurnRows + lrow[u], (p.col0 + col[u]) >> 3), v[u]);
-#pragma unroll
-            for (int u = 0; u < St::kTurn; ++u) {
-                const int row = top + turn * St::kTurnRows + lrow[u];
-                if (row >= p.M)
-                    continue;
-                const int m = hold_v(n[u]);
-                char *const to = element_at(p.y, row * p.ldy + col[u], ye);
-                if (p.y_f32) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t a = now[u].a[e], b = now[u].b[e];
-                        v[u][e] += __builtin_bit_cast(float, a);
-                        v[u][4 + e] += __builtin_bit_cast(float, b);
-                    }
-                    store8_32(to, m, v[u]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[u][2 * e] += T::low(now[u].a[e]);
-                        v[u][2 * e + 1] += T::high(now[u].a[e]);
-                    }
-                    store8_16<T>(to, m, v[u]);
-                }
-            }
-        }
-        lanes_in_step();   // the next pass overwrites these rows
-    }
+    if (row0 + 16 * kB <= p.M && col0 + 16 * kB <= p.N)
+        Epilogue<T, kB, true>(p, mine, loop.lane, row0, col0).run(acc);
+    else
+        Epilogue<T, kB, false>(p, mine, loop.lane, row0, col0).run(acc);
 }
 
 template <class T, class Mma, int kT>
