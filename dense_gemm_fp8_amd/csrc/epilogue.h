@@ -30,16 +30,31 @@ struct TypeF16 {
 // Eight consecutive values of a row.  Rows start anywhere that suits their element:
 // the hardware takes 16-byte accesses at any address.
 typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ u32x4_t load16(const void *p) { return *static_cast<const u32x4_any_t *>(p); }
-__device__ __forceinline__ void store16(void *p, const u32x4_t &v) { *static_cast<u32x4_any_t *>(p) = v; }
+// kStream: lines that nothing reads again soon, which then leave the L2 first.
+template <bool kStream = false>
+__device__ __forceinline__ u32x4_t load16(const void *p)
+{
+    if constexpr (kStream)
+        return __builtin_nontemporal_load(static_cast<const u32x4_any_t *>(p));
+    else
+        return *static_cast<const u32x4_any_t *>(p);
+}
+template <bool kStream>
+__device__ __forceinline__ void store16(void *p, const u32x4_t &v)
+{
+    if constexpr (kStream)
+        __builtin_nontemporal_store((u32x4_any_t)v, static_cast<u32x4_any_t *>(p));
+    else
+        *static_cast<u32x4_any_t *>(p) = v;
+}
 
 // The first n of the eight elements from p (n < 1: none), the rest zeros.
-template <class T>
+template <class T, bool kStream = false>
 __device__ __forceinline__ void load8_16(const void *p, int n, float (&v)[8])
 {
     u32x4_t w = {0u, 0u, 0u, 0u};
     if (n >= 8) {
-        w = load16(p);
+        w = load16<kStream>(p);
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
@@ -72,12 +87,12 @@ __device__ __forceinline__ void load8_32(const void *p, int n, float (&v)[8])
         v[4 + e] = __builtin_bit_cast(float, y);
     }
 }
-template <class T>
+template <class T, bool kStream = false>
 __device__ __forceinline__ void store8_16(void *p, int n, const float (&v)[8])
 {
     const u32x4_t w = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])};
     if (n >= 8) {
-        store16(p, w);
+        store16<kStream>(p, w);
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
@@ -85,6 +100,7 @@ __device__ __forceinline__ void store8_16(void *p, int n, const float (&v)[8])
                 static_cast<uint16_t *>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
 }
+template <bool kStream = false>
 __device__ __forceinline__ void store8_32(void *p, int n, const float (&v)[8])
 {
     float *f = static_cast<float *>(p);
@@ -95,8 +111,8 @@ __device__ __forceinline__ void store8_32(void *p, int n, const float (&v)[8])
             a[e] = __builtin_bit_cast(uint32_t, v[e]);
             b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
         }
-        store16(f, a);
-        store16(f + 4, b);
+        store16<kStream>(f, a);
+        store16<kStream>(f + 4, b);
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)

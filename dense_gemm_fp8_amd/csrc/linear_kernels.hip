@@ -13,12 +13,68 @@ namespace hkg {
 namespace {
 
 // ---- dropout ----------------------------------------------------------------------
-// A workgroup is 2^s lanes of 8 columns wide, 2^s near a row's groups but at most 256,
-// and takes kRows rows a lane; a lane's loads are all sent before the first is used.
+// A lane takes 16 bytes of the result's rows, 8 columns or 4 of fp32, so that a wave's
+// accesses are whole lines; a workgroup is 2^s lanes wide, 2^s near a row's but at most
+// 256, and takes kDropRows rows a lane, whose loads are all sent before the first is used.
+// Bound by its bytes: TB/s here means read and written.
 constexpr int kDropRows = 4;
 
-template <class T, int kXBits, int kOutBits>
-__global__ __launch_bounds__(256) void dropout_kernel(const DropoutCall p, int shift)
+// Four values of 16 or 32 bits, the first n of them.
+template <class T, int kBits>
+__device__ __forceinline__ void load4(const void *p, int n, float (&v)[4])
+{
+    typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+    if constexpr (kBits == 16) {
+        u32x2_t w = {0u, 0u};
+        if (n >= 4) {
+            w = __builtin_nontemporal_load(static_cast<const u32x2_any_t *>(p));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < n)
+                    w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            v[2 * e] = T::low(w[e]);
+            v[2 * e + 1] = T::high(w[e]);
+        }
+    } else {
+        u32x4_t w = {0u, 0u, 0u, 0u};
+        if (n >= 4) {
+            w = load16<true>(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < n)
+                    w[e] = static_cast<const uint32_t *>(p)[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = w[e];
+            v[e] = __builtin_bit_cast(float, x);
+        }
+    }
+}
+__device__ __forceinline__ void store4(float *p, int n, const float (&v)[4])
+{
+    if (n >= 4) {
+        u32x4_t w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = __builtin_bit_cast(uint32_t, v[e]);
+        store16<true>(p, w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n)
+                p[e] = v[e];
+    }
+}
+
+// Results of 16 bits: a lane's 8 columns are one call of the generator.
+template <class T>
+__global__ __launch_bounds__(256) void dropout16_kernel(const DropoutCall p, int shift)
 {
     const int wide = 1 << shift, tall = 256 >> shift;
     const int group = blockIdx.x * wide + (threadIdx.x & (wide - 1)), col = 8 * group, n = p.cols - col;
@@ -32,18 +88,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(const DropoutCall p, int s
         for (int i = 0; i < kDropRows; ++i) {
             const int64_t row = row0 + i * tall;
             const int m = row < p.rows ? n : 0;
-            const char *const from = element_at(p.x, row * p.ldx + col, kXBits / 8);
-            if constexpr (kXBits == 16)
-                load8_16<T>(from, m, v[i]);
-            else
-                load8_32(from, m, v[i]);
-            if (p.residual) {
-                const char *const add = element_at(p.residual, row * p.ldr + col, kOutBits / 8);
-                if constexpr (kOutBits == 16)
-                    load8_16<T>(add, m, r[i]);
-                else
-                    load8_32(add, m, r[i]);
-            }
+            load8_16<T, true>(element_at(p.x, row * p.ldx + col, 2), m, v[i]);
+            if (p.residual)
+                load8_16<T, true>(element_at(p.residual, row * p.ldr + col, 2), m, r[i]);
         }
 #pragma unroll
         for (int i = 0; i < kDropRows; ++i) {
@@ -56,11 +103,56 @@ __global__ __launch_bounds__(256) void dropout_kernel(const DropoutCall p, int s
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[i][e] += r[i][e];
-            char *const to = element_at(p.out, row * p.ldo + col, kOutBits / 8);
-            if constexpr (kOutBits == 16)
-                store8_16<T>(to, n, v[i]);
-            else
-                store8_32(to, n, v[i]);
+            store8_16<T, true>(element_at(p.out, row * p.ldo + col, 2), n, v[i]);
+        }
+    }
+}
+
+// Results of 32 bits: a lane's 4 columns are half a call.  Two neighbours share a group of
+// 8; the even one calls the generator for one row of each two, the odd one for the other,
+// and they exchange the halves.  (With 8 columns a lane, in two accesses of half lines
+// each: 8192 x 14336 170 us, and 185 with stores that leave the L2 first.)
+template <class T, int kXBits>
+__global__ __launch_bounds__(256) void dropout32_kernel(const DropoutCall p, int shift)
+{
+    const int wide = 1 << shift, tall = 256 >> shift;        // wide at least 2
+    const int unit = blockIdx.x * wide + (threadIdx.x & (wide - 1)), col = 4 * unit, n = p.cols - col;
+    const bool odd = unit & 1;
+    const Key key(p.drop);
+    for (int64_t top = (int64_t)blockIdx.y * (tall * kDropRows); top < p.rows; top += (int64_t)gridDim.y * (tall * kDropRows)) {
+        const int64_t row0 = top + (threadIdx.x >> shift);
+        float v[kDropRows][4], r[kDropRows][4];
+#pragma unroll
+        for (int i = 0; i < kDropRows; ++i) {
+            const int64_t row = row0 + i * tall;
+            const int m = row < p.rows ? n : 0;
+            load4<T, kXBits>(element_at(p.x, row * p.ldx + col, kXBits / 8), m, v[i]);
+            if (p.residual)
+                load4<T, 32>(element_at(p.residual, row * p.ldr + col, 4), m, r[i]);
+        }
+        if (p.drop.below > 0)
+#pragma unroll
+            for (int i = 0; i < kDropRows; i += 2) {         // every lane, so that its neighbour gets its half
+                const u32x4_t w = key.numbers((int)(row0 + (i + odd) * tall), unit >> 1);
+                const uint32_t a = quad_xor<0xB1>(odd ? w[0] : w[2]), b = quad_xor<0xB1>(odd ? w[1] : w[3]);
+                const uint32_t n0[2] = {odd ? a : w[0], odd ? b : w[1]}, n1[2] = {odd ? w[2] : a, odd ? w[3] : b};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int s = 16 * (e & 1);
+                    v[i][e] = (n0[e >> 1] >> s & 0xffffu) >= p.drop.below ? v[i][e] * p.drop.scale : 0.0f;
+                    v[i + 1][e] = (n1[e >> 1] >> s & 0xffffu) >= p.drop.below ? v[i + 1][e] * p.drop.scale : 0.0f;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kDropRows; ++i) {
+            const int64_t row = row0 + i * tall;
+            if (row >= p.rows)
+                continue;
+            if (p.residual)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[i][e] += r[i][e];
+            store4(reinterpret_cast<float *>(element_at(p.out, row * p.ldo + col, 4)), n, v[i]);
         }
     }
 }
@@ -264,7 +356,7 @@ __global__ __launch_bounds__(256) void linear_prepare_kernel(const PrepareParams
         }
         const u32x4_t w = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])};
         if (to && row < rows && c < cols)
-            store16(to + row * ld + c, w);                  // rows of whole groups: zeros past the last column
+            store16<false>(to + row * ld + c, w);                  // rows of whole groups: zeros past the last column
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint32_t *>(&tile[rl * kPrepPitch + 8 * g + 2 * e]) = w[e];
@@ -284,7 +376,7 @@ __global__ __launch_bounds__(256) void linear_prepare_kernel(const PrepareParams
             for (int e = 0; e < 4; ++e)
                 w[e] = tile[(8 * g + 2 * e) * kPrepPitch + cl] | (uint32_t)tile[(8 * g + 2 * e + 1) * kPrepPitch + cl] << 16;
             if (col < cols && row < rows)
-                store16(to_t + col * ld_t + row, w);        // rows past the matrix are zeros in the tile
+                store16<false>(to_t + col * ld_t + row, w);        // rows past the matrix are zeros in the tile
         }
     }
     if (what == 0 && p.sums && threadIdx.x < kPrep && c0 + (int)threadIdx.x < cols) {
@@ -332,31 +424,39 @@ hipError_t few_rows_of(const LinearParams &p, hipStream_t stream)
     return few_rows<T, 4, 2>(p, blocks, stream);
 }
 
-template <class T, int kXBits, int kOutBits>
-hipError_t dropout_of(const DropoutCall &p, hipStream_t stream)
+// f(grid, shift): shapes a launch whose lanes take `cols` columns of a row each.
+template <class F>
+hipError_t dropout_shape(const DropoutCall &p, int cols, F &&f)
 {
-    const int groups = (p.cols + 7) / 8;
-    int shift = 0;
-    while (shift < 8 && (1 << shift) < groups)
+    const int64_t units = ((int64_t)p.cols + cols - 1) / cols;
+    int shift = cols == 4 ? 1 : 0;
+    while (shift < 8 && (1 << shift) < units)
         ++shift;
-    const int64_t tall = (256 >> shift) * kDropRows, high = (p.rows + tall - 1) / tall, wide = (groups + (1 << shift) - 1) >> shift;
+    const int64_t tall = (256 >> shift) * kDropRows, high = (p.rows + tall - 1) / tall, wide = (units + (1 << shift) - 1) >> shift;
     // at most 2^23 workgroups, so that their threads stay below 2^32; more rows in turns
-    int64_t turn = (int64_t(1) << 23) / wide;               // wide is at most 2^20
+    int64_t turn = (int64_t(1) << 23) / wide;               // wide is at most 2^21
     turn = turn < 65535 ? turn : 65535;
-    const dim3 grid((unsigned)wide, (unsigned)(high < turn ? high : turn));
-    hipLaunchKernelGGL((dropout_kernel<T, kXBits, kOutBits>), grid, dim3(256), 0, stream, p, shift);
+    f(dim3((unsigned)wide, (unsigned)(high < turn ? high : turn)), shift);
     return hipGetLastError();
+}
+template <class T>
+hipError_t dropout_of(int x_bits, int out_bits, const DropoutCall &p, hipStream_t stream)
+{
+    return dropout_shape(p, out_bits == 16 ? 8 : 4, [&](dim3 grid, int shift) {
+        if (out_bits == 16)
+            hipLaunchKernelGGL(dropout16_kernel<T>, grid, dim3(256), 0, stream, p, shift);
+        else if (x_bits == 16)
+            hipLaunchKernelGGL((dropout32_kernel<T, 16>), grid, dim3(256), 0, stream, p, shift);
+        else
+            hipLaunchKernelGGL((dropout32_kernel<TypeBf16, 32>), grid, dim3(256), 0, stream, p, shift);
+    });
 }
 
 }  // namespace
 
 hipError_t launch_dropout(bool f16, int x_bits, int out_bits, const DropoutCall &p, hipStream_t stream)
 {
-    if (x_bits == 32)
-        return dropout_of<TypeBf16, 32, 32>(p, stream);
-    if (f16)
-        return out_bits == 32 ? dropout_of<TypeF16, 16, 32>(p, stream) : dropout_of<TypeF16, 16, 16>(p, stream);
-    return out_bits == 32 ? dropout_of<TypeBf16, 16, 32>(p, stream) : dropout_of<TypeBf16, 16, 16>(p, stream);
+    return f16 ? dropout_of<TypeF16>(x_bits, out_bits, p, stream) : dropout_of<TypeBf16>(x_bits, out_bits, p, stream);
 }
 
 // A launch's threads have to stay below 2^32, or part of the grid is left out without an
