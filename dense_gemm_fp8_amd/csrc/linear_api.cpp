@@ -53,15 +53,43 @@ int check_operand(const void *p, int64_t rows, int64_t cols, int64_t *ld)
 // Whether out may share its bytes with the input at `in`: the same matrix, element for element.
 bool same_matrix(const void *out, int64_t ldo, const void *in, int64_t ldi) { return out == in && ldo == ldi; }
 
-// The product and its epilogue, on arguments that are checked.  Up to 512 blocks of 64 x
-// 32 results (two for each compute unit) the kernel for few rows, which splits K over a
-// workgroup's waves; above, the launches that the bf16 GEMM makes of this shape.
-hipError_t run_linear(bool f16, const hkg::LinearParams &p, hipStream_t stream)
+// How a product runs: the kernel for few rows, 128-tiles with K over `splits` workgroups
+// of `steps` K steps each, or tiles.
+struct How {
+    enum Kind { kFewRows, kSplit, kTiles } kind;
+    int splits, steps;
+};
+// `transposed`: the operands may have K along their rows (gradients), which only tiles take.
+How how_to(int64_t M, int64_t N, int64_t K, bool transposed)
 {
-    if (p.K == 0 || p.M <= 16 || ceil_div(p.M, 64) * ceil_div(p.N, 32) <= 512)
+    const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), steps = ceil_div(K, 64);
+    if (K == 0 || (!transposed && M <= 16) || ceil_div(M, 64) * ceil_div(N, 32) <= 512)
+        return {How::kFewRows, 0, 0};
+    if (tiles <= 256 && steps >= 16) {
+        const int64_t splits = 512 / tiles < steps / 8 ? 512 / tiles : steps / 8, each = ceil_div(steps, splits);
+        return {How::kSplit, static_cast<int>(ceil_div(steps, each)), static_cast<int>(each)};
+    }
+    return {How::kTiles, 0, 0};
+}
+int64_t parts_bytes(const How &h, int64_t M, int64_t N)
+{
+    return h.kind == How::kSplit ? hkg::linear_parts_bytes(M, N, h.splits) : 0;
+}
+
+// The product and its epilogue, on arguments that are checked.
+hipError_t run_product(bool f16, const How &h, const hkg::LinearParams &p, void *parts, hipStream_t stream)
+{
+    if (h.kind == How::kFewRows)
         return hkg::launch_linear_few_rows(f16, p, stream);
+    if (h.kind == How::kSplit) {
+        const hkg::TileOrder o = order_of(p.M, p.N, 2 * static_cast<int64_t>(p.K), 128);
+        return hkg::launch_linear_split(f16, {128, o.Gm, o.Gn, o.W, o.C}, h.splits, h.steps, static_cast<float *>(parts), p, stream);
+    }
+    // the launches that the GEMM makes of this shape; operands with K along their rows have
+    // no 192-tiles, as MXFP8 has none
     Plan pl;
-    if (plan_gemm(hkg::kBf16, p.M, p.N, p.K, nullptr, &pl) != HKG_OK)
+    const bool transposed = p.tr_a || p.tr_b;
+    if (plan_gemm(transposed ? hkg::kMx : hkg::kBf16, p.M, p.N, transposed ? 2 * static_cast<int64_t>(p.K) : p.K, nullptr, &pl) != HKG_OK)
         return hipErrorInvalidValue;
     hipError_t e = hipSuccess;
     int64_t row = 0;
@@ -77,17 +105,24 @@ hipError_t run_linear(bool f16, const hkg::LinearParams &p, hipStream_t stream)
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 constexpr int64_t kSumRows = 64;   // rows of dz whose sum is one row of partial sums
 
-// Workspace of the gradients, in this order.
+// How the gradients' products run, and their workspace: what they read that is formed
+// first, whose parts are in this order, and room for the parts of split products.
 struct BackwardLayout {
-    int64_t dz, dzt, wt, xt, sums, total;
+    How x, w;                                    // dx, dw
+    int64_t dz, dzt, wt, xt, sums, parts, total;
     BackwardLayout(int64_t M, int64_t N, int64_t K)
     {
+        x = how_to(M, K, N, true);
+        w = how_to(N, K, M, true);
+        // the kernel for few rows takes transposed copies, tiles the matrices themselves
         dz = 0;
         dzt = dz + 2 * M * round8(N);
-        wt = dzt + 2 * N * round8(M);
-        xt = wt + 2 * K * round8(N);
-        sums = xt + 2 * K * round8(M);
-        total = sums + round16(4 * ceil_div(M, kSumRows) * N);
+        wt = dzt + (w.kind == How::kFewRows ? 2 * N * round8(M) : 0);
+        xt = wt + (x.kind == How::kFewRows ? 2 * K * round8(N) : 0);
+        sums = xt + (w.kind == How::kFewRows ? 2 * K * round8(M) : 0);
+        parts = sums + round16(4 * ceil_div(M, kSumRows) * N);
+        const int64_t px = parts_bytes(x, M, K), pw = parts_bytes(w, N, K);
+        total = parts + (px > pw ? px : pw);
     }
 };
 // Operands of the gradients' products are M, N and K long, and their preparation is one
@@ -161,7 +196,7 @@ int64_t hkg_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
         return HKG_ERR_SHAPE;
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) / (kTile * 2))
         return HKG_ERR_SIZE;
-    return 0;
+    return M == 0 || N == 0 ? 0 : parts_bytes(how_to(M, N, K, false), M, N);
 }
 
 int hkg_linear(int64_t M, int64_t N, int64_t K, int32_t type, const void *x, int64_t ldx,
@@ -243,7 +278,7 @@ int hkg_linear(int64_t M, int64_t N, int64_t K, int32_t type, const void *x, int
     p.bias_f32 = e.bias_type == HKG_T_F32;
     p.y_f32 = y_type == HKG_T_F32;
     p.act = e.activation;
-    return launched(run_linear(type == HKG_T_F16, p, static_cast<hipStream_t>(stream)));
+    return launched(run_product(type == HKG_T_F16, how_to(M, N, K, false), p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 int64_t hkg_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K)
@@ -335,10 +370,11 @@ int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const voi
         p.ldz = ldz;
         p.ldx = ldx;
         p.ldw = ldw;
-        p.dz = want_x ? reinterpret_cast<uint16_t *>(ws + at.dz) : nullptr;
-        p.dzt = want_w ? reinterpret_cast<uint16_t *>(ws + at.dzt) : nullptr;
-        p.wt = want_x ? reinterpret_cast<uint16_t *>(ws + at.wt) : nullptr;
-        p.xt = want_w ? reinterpret_cast<uint16_t *>(ws + at.xt) : nullptr;
+        const bool few_x = want_x && at.x.kind == How::kFewRows, few_w = want_w && at.w.kind == How::kFewRows;
+        p.dz = want_x || (want_w && !few_w) ? reinterpret_cast<uint16_t *>(ws + at.dz) : nullptr;
+        p.dzt = few_w ? reinterpret_cast<uint16_t *>(ws + at.dzt) : nullptr;
+        p.wt = few_x ? reinterpret_cast<uint16_t *>(ws + at.wt) : nullptr;
+        p.xt = few_w ? reinterpret_cast<uint16_t *>(ws + at.xt) : nullptr;
         p.sums = want_b ? reinterpret_cast<float *>(ws + at.sums) : nullptr;
         p.M = static_cast<int>(M);
         p.N = static_cast<int>(N);
@@ -349,27 +385,30 @@ int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const voi
     }
     hkg::LinearParams q = {};
     q.drop = {0, 1.0f, 0, 0, nullptr};
+    q.N = static_cast<int>(K);
     if (rc == HKG_OK && want_x) {
         q.A = p.dz;
-        q.B = p.wt;
-        q.lda = q.ldb = round8(N);
+        q.lda = round8(N);
+        q.tr_b = at.x.kind != How::kFewRows;
+        q.B = q.tr_b ? static_cast<const uint16_t *>(W) : p.wt;
+        q.ldb = q.tr_b ? ldw : round8(N);
         q.M = static_cast<int>(M);
-        q.N = static_cast<int>(K);
-        q.K = static_cast<int>(round8(N));
+        q.K = static_cast<int>(q.tr_b ? N : round8(N));
         q.y = dx;
         q.ldy = lddx;
-        rc = launched(run_linear(f16, q, st));
+        rc = launched(run_product(f16, at.x, q, ws + at.parts, st));
     }
     if (rc == HKG_OK && want_w) {
-        q.A = p.dzt;
-        q.B = p.xt;
-        q.lda = q.ldb = round8(M);
+        q.tr_a = q.tr_b = at.w.kind != How::kFewRows;
+        q.A = q.tr_a ? p.dz : p.dzt;
+        q.lda = q.tr_a ? round8(N) : round8(M);
+        q.B = q.tr_b ? static_cast<const uint16_t *>(x) : p.xt;
+        q.ldb = q.tr_b ? ldx : round8(M);
         q.M = static_cast<int>(N);
-        q.N = static_cast<int>(K);
-        q.K = static_cast<int>(round8(M));
+        q.K = static_cast<int>(q.tr_a ? M : round8(M));
         q.y = dw;
         q.ldy = lddw;
-        rc = launched(run_linear(f16, q, st));
+        rc = launched(run_product(f16, at.w, q, ws + at.parts, st));
     }
     if (rc == HKG_OK && want_b)
         rc = launched(hkg::launch_linear_bias_sum(p.sums, static_cast<int>(ceil_div(M, kSumRows)),

@@ -85,7 +85,9 @@ struct RowPtr {
 //
 // From accumulators to results: the quarter's rows in passes of what LDS holds, a pass in
 // turns of kTurn groups of 8 columns a lane.  kWhole: the quarter lies inside the matrix.
-template <class T, int kB, bool kWhole>
+// kTrB: B is transposed, whose blocks are 16 consecutive columns, and the product is one of
+// the gradients', whose results go out as they are in 16 bits.
+template <class T, int kB, bool kWhole, bool kTrB>
 struct Epilogue {
     using St = F32Stage<kB>;
     const LinearParams &p;
@@ -105,12 +107,12 @@ struct Epilogue {
 #pragma unroll
         for (int u = 0; u < St::kTurn; ++u)
             col[u] = col0 + 8 * ((64 * u + lane) % St::kLanes);
-        y.init(p.y, p.ldy, p.y_f32 ? 4 : 2, row0, col0, lane);
-        if (p.z)
+        y.init(p.y, p.ldy, !kTrB && p.y_f32 ? 4 : 2, row0, col0, lane);
+        if (!kTrB && p.z)
             z.init(p.z, p.ldz, 2, row0, col0, lane);
-        if (p.residual)
+        if (!kTrB && p.residual)
             r.init(p.residual, p.ldr, p.y_f32 ? 4 : 2, row0, col0, lane);
-        if (p.bias)
+        if (!kTrB && p.bias)
 #pragma unroll
             for (int u = 0; u < St::kTurn; ++u) {
                 if (St::kAligned && u > 0) {
@@ -131,7 +133,7 @@ struct Epilogue {
     // The residual's values of a turn, and on to the next.
     __device__ __forceinline__ void fetch(int turn)
     {
-        if (!p.residual || turn >= St::kPasses * St::kTurns)
+        if (kTrB || !p.residual || turn >= St::kPasses * St::kTurns)
             return;
 #pragma unroll
         for (int u = 0; u < St::kTurn; ++u) {
@@ -178,32 +180,33 @@ struct Epilogue {
         for (int u = 0; u < St::kTurn; ++u)
             now[u] = next[u];
         fetch(turn + 1);
-        if (p.bias)
+        if (!kTrB && p.bias)
 #pragma unroll
             for (int u = 0; u < St::kTurn; ++u)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     v[u][e] += bias[u][e];
-        if (p.z) {
+        if (!kTrB && p.z) {
 #pragma unroll
             for (int u = 0; u < St::kTurn; ++u)
                 if (inside(turn, u))
                     store8_16<T, true>(z.get(u), columns(u), v[u]);
             z.next();
         }
-        with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
-#pragma unroll
-            for (int u = 0; u < St::kTurn; ++u)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[u][e] = act_of<decltype(a)::value>(v[u][e]);
-        });
-        if (p.drop.below > 0)
+        if constexpr (!kTrB)
+            with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
+    #pragma unroll
+                for (int u = 0; u < St::kTurn; ++u)
+    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[u][e] = act_of<decltype(a)::value>(v[u][e]);
+            });
+        if (!kTrB && p.drop.below > 0)
 #pragma unroll
             for (int u = 0; u < St::kTurn; ++u)
                 drop8(p.drop, key.numbers(p.row0 + row0 + row_of(turn, u), (p.col0 + col[u]) >> 3), v[u]);
-        if (p.y_f32) {
-            if (p.residual)
+        if (!kTrB && p.y_f32) {
+            if (!kTrB && p.residual)
 #pragma unroll
                 for (int u = 0; u < St::kTurn; ++u)
 #pragma unroll
@@ -217,7 +220,7 @@ struct Epilogue {
                 if (inside(turn, u))
                     store8_32<true>(y.get(u), columns(u), v[u]);
         } else {
-            if (p.residual)
+            if (!kTrB && p.residual)
 #pragma unroll
                 for (int u = 0; u < St::kTurn; ++u)
 #pragma unroll
@@ -238,9 +241,9 @@ struct Epilogue {
         const int x = lane & 15, q = lane >> 4;
         int to[kB];                                          // LDS address of the lane's unit of column block j
 #pragma unroll
-        for (int j = 0; j < kB; ++j)                         // columns 32 (j / 2) + 8 q + 4 (j % 2) ..
+        for (int j = 0; j < kB; ++j)                         // columns 32 (j / 2) + 8 q + 4 (j % 2) .., or 16 j + 4 q ..
             to[j] = (int)(uintptr_t)(__attribute__((address_space(3))) char *)mine +
-                    St::place(x, 8 * (j >> 1) + 2 * q + (j & 1));
+                    St::place(x, kTrB ? 4 * j + q : 8 * (j >> 1) + 2 * q + (j & 1));
         fetch(0);
         for (int pass = 0; pass < St::kPasses; ++pass) {
             slots<St::kPasses>([&](auto which) __attribute__((always_inline)) {
@@ -260,20 +263,27 @@ struct Epilogue {
     }
 };
 
-template <class T, class Mma, int kT>
-__device__ __forceinline__ void linear_tile(const TileOperands &o, const LinearParams &p, int block, char *smem)
+template <int kB>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[kB][kB])
 {
-    using Loop = TileLoop<Mma, kT>;
-    constexpr int kB = Loop::kB;
-    static_assert(4 * F32Stage<kB>::kBytes <= Loop::kLds, "the stage fits");
-    int tm, tn;
-    remap_tile(block, o.Gm, o.Gn, o.W, o.C, tm, tn);
-    f32x4_t acc[kB][kB];
 #pragma unroll
     for (int i = 0; i < kB; ++i)
 #pragma unroll
         for (int j = 0; j < kB; ++j)
             acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+}
+
+template <class T, class Mma, int kT, bool kTrA, bool kTrB>
+__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void linear_tile_kernel(const TransposableOperands o, const LinearParams p)
+{
+    using Loop = TileLoop<Mma, kT, kTrA, kTrB>;
+    constexpr int kB = Loop::kB;
+    static_assert(4 * F32Stage<kB>::kBytes <= Loop::kLds, "the stage fits");
+    __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
+    int tm, tn;
+    remap_tile(blockIdx.x, o.Gm, o.Gn, o.W, o.C, tm, tn);
+    f32x4_t acc[kB][kB];
+    clear(acc);
     Loop loop;
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
@@ -283,26 +293,127 @@ __device__ __forceinline__ void linear_tile(const TileOperands &o, const LinearP
     char *const mine = smem + loop.wave * F32Stage<kB>::kBytes;
     barrier();   // every wave has read its last fragments
     if (row0 + 16 * kB <= p.M && col0 + 16 * kB <= p.N)
-        Epilogue<T, kB, true>(p, mine, loop.lane, row0, col0).run(acc);
+        Epilogue<T, kB, true, kTrB>(p, mine, loop.lane, row0, col0).run(acc);
     else
-        Epilogue<T, kB, false>(p, mine, loop.lane, row0, col0).run(acc);
+        Epilogue<T, kB, false, kTrB>(p, mine, loop.lane, row0, col0).run(acc);
 }
 
-template <class T, class Mma, int kT>
-__global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void linear_tile_kernel(const TileOperands o, const LinearParams p)
+// ---- K over several workgroups ----------------------------------------------------------
+// For grids of 128-tiles that would leave compute units idle.  Part s of a tile has K steps
+// steps s .. and writes its sums in an order of its own, whole KiB a store: of a wave's
+// quarter, 16 x 32 blocks (i, h), of a block the units of columns 4 (j & 1) .. in turn, of
+// those lane 16 q + x's four columns 8 q + 4 (j & 1) .. of row x.
+constexpr int kPartQuarter = 64 * 64;   // floats
+
+template <class Mma, bool kTrA, bool kTrB>
+__global__ __launch_bounds__(256, 2) void linear_part_kernel(const TransposableOperands all, int steps, float *parts)
 {
-    __shared__ __attribute__((aligned(1024))) char smem[TileLoop<Mma, kT>::kLds];
-    linear_tile<T, Mma, kT>(o, p, blockIdx.x, smem);
+    using Loop = TileLoop<Mma, 128, kTrA, kTrB>;
+    constexpr int kB = Loop::kB;
+    __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
+    const int tiles = all.Gm * all.Gn, split = blockIdx.x / tiles, block = blockIdx.x % tiles, k0 = split * steps;
+    TransposableOperands o = all;
+    o.A = static_cast<const char *>(o.A) + (int64_t)k0 * (kTrA ? 64 * (int64_t)o.pitch_a : kStepBytes);
+    o.B = static_cast<const char *>(o.B) + (int64_t)k0 * (kTrB ? 64 * (int64_t)o.pitch_b : kStepBytes);
+    o.nk = min(steps, all.nk - k0);
+    o.kb = min(steps * kStepBytes, all.kb - k0 * kStepBytes);
+    o.kt = min(steps * 64, all.kt - k0 * 64);
+    int tm, tn;
+    remap_tile(block, o.Gm, o.Gn, o.W, o.C, tm, tn);
+    f32x4_t acc[kB][kB];
+    clear(acc);
+    Loop loop;
+    loop.init(o, smem, tm, tn);
+    loop.run(acc, o.nk);
+    settle(acc);
+    float *const to = parts + ((int64_t)split * tiles + (int64_t)tm * o.Gn + tn) * (4 * kPartQuarter) + loop.wave * kPartQuarter;
+    const int x = loop.lane & 15, q = loop.lane >> 4;
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j) {
+            // transposed B: unit 4 j + q of 4 columns instead of 8 (j / 2) + 2 q + j % 2
+            const int jj = kTrB ? 2 * (j >> 1) + (q & 1) : j, qq = kTrB ? 2 * (j & 1) + (q >> 1) : q;
+            *reinterpret_cast<f32x4_t *>(to + ((i * kB + jj) * 64 + 16 * qq + x) * 4) = acc[i][j];
+        }
 }
 
-TileOperands operands(const TileGrid &g, const LinearParams &p)
+// A wave joins one 16 x 32 block: a lane has 8 columns of a row.
+template <class T>
+__global__ __launch_bounds__(256) void linear_join_kernel(const LinearParams p, int Gn, int tiles, int splits, const float *parts)
 {
-    TileOperands o = {};
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, x = lane & 15, q = lane >> 4;
+    const int unit = 4 * blockIdx.x + wave;                  // of tiles x 4 quarters x 8 blocks
+    const int tile = unit >> 5, quarter = (unit >> 3) & 3, i = (unit >> 1) & 3, h = unit & 1;
+    const int row = 128 * (tile / Gn) + 64 * (quarter >> 1) + 16 * i + x, col = 128 * (tile % Gn) + 64 * (quarter & 1) + 32 * h + 8 * q;
+    const int n = row < p.M ? p.N - col : 0;
+    const float *from = parts + (int64_t)tile * (4 * kPartQuarter) + quarter * kPartQuarter + ((i * 4 + 2 * h) * 64 + lane) * 4;
+    const int64_t stride = (int64_t)tiles * (4 * kPartQuarter);
+    if (n <= 0)
+        return;
+    const int ye = p.y_f32 ? 4 : 2;
+    float r[8];
+    if (p.residual) {
+        if (p.y_f32)
+            load8_32(element_at(p.residual, row * p.ldr + col, 4), n, r);
+        else
+            load8_16<T>(element_at(p.residual, row * p.ldr + col, 2), n, r);
+    }
+    f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    int s = 0;
+    for (; s + 4 <= splits; s += 4) {
+        f32x4_t a[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[k] = *reinterpret_cast<const f32x4_t *>(from + (s + k) * stride);
+            b[k] = *reinterpret_cast<const f32x4_t *>(from + (s + k) * stride + 256);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            lo += a[k];
+            hi += b[k];
+        }
+    }
+    for (; s < splits; ++s) {
+        lo += *reinterpret_cast<const f32x4_t *>(from + s * stride);
+        hi += *reinterpret_cast<const f32x4_t *>(from + s * stride + 256);
+    }
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    if (p.bias) {
+        float b[8];
+        if (p.bias_f32)
+            load8_32(element_at(p.bias, col, 4), n, b);
+        else
+            load8_16<T>(element_at(p.bias, col, 2), n, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += b[e];
+    }
+    if (p.z)
+        store8_16<T>(element_at(p.z, row * p.ldz + col, 2), n, v);
+    act8(p.act, v);
+    if (p.drop.below > 0)
+        drop8(p.drop, Key(p.drop).numbers(p.row0 + row, (p.col0 + col) >> 3), v);
+    if (p.residual)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += r[e];
+    char *const to = element_at(p.y, row * p.ldy + col, ye);
+    if (p.y_f32)
+        store8_32(to, n, v);
+    else
+        store8_16<T>(to, n, v);
+}
+
+TransposableOperands operands(const TileGrid &g, const LinearParams &p)
+{
+    TransposableOperands o = {};
     o.A = p.A;
     o.B = p.B;
     o.pitch_a = (int)(2 * p.lda);
     o.pitch_b = (int)(2 * p.ldb);
-    o.kb = 2 * p.K;
+    o.kb = 2 * ((p.K + 7) & ~7);
+    o.kt = p.K;
     o.rows_a = p.M;
     o.rows_b = p.N;
     o.Gm = g.Gm;
@@ -313,17 +424,45 @@ TileOperands operands(const TileGrid &g, const LinearParams &p)
     return o;
 }
 
-template <class T, class Mma>
+template <class T, class Mma, bool kTrA, bool kTrB>
 hipError_t tiles_of(const TileGrid &g, const LinearParams &p, hipStream_t stream)
 {
-    const TileOperands o = operands(g, p);
+    const TransposableOperands o = operands(g, p);
     const dim3 grid((unsigned)g.Gm * (unsigned)g.Gn), block(256);
     if (g.tile == 256)
-        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 256>), grid, block, 0, stream, o, p);
-    else if (g.tile == 192)
-        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 192>), grid, block, 0, stream, o, p);
+        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 256, kTrA, kTrB>), grid, block, 0, stream, o, p);
+    else if (g.tile == 128)
+        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 128, kTrA, kTrB>), grid, block, 0, stream, o, p);
+    else if constexpr (!kTrA && !kTrB)
+        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 192, false, false>), grid, block, 0, stream, o, p);
     else
-        hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 128>), grid, block, 0, stream, o, p);
+        return hipErrorInvalidValue;
+    return hipGetLastError();
+}
+template <class T, class Mma>
+hipError_t tiles_as(const TileGrid &g, const LinearParams &p, hipStream_t stream)
+{
+    return p.tr_a ? tiles_of<T, Mma, true, true>(g, p, stream)
+         : p.tr_b ? tiles_of<T, Mma, false, true>(g, p, stream)
+                  : tiles_of<T, Mma, false, false>(g, p, stream);
+}
+
+template <class T, class Mma>
+hipError_t split_of(const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p, hipStream_t stream)
+{
+    const TransposableOperands o = operands(g, p);
+    const int tiles = g.Gm * g.Gn;
+    const dim3 grid((unsigned)tiles * (unsigned)splits), block(256);
+    if (p.tr_a)
+        hipLaunchKernelGGL((linear_part_kernel<Mma, true, true>), grid, block, 0, stream, o, steps, parts);
+    else if (p.tr_b)
+        hipLaunchKernelGGL((linear_part_kernel<Mma, false, true>), grid, block, 0, stream, o, steps, parts);
+    else
+        hipLaunchKernelGGL((linear_part_kernel<Mma, false, false>), grid, block, 0, stream, o, steps, parts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(linear_join_kernel<T>, dim3(8u * (unsigned)tiles), block, 0, stream, p, g.Gn, tiles, splits, parts);
     return hipGetLastError();
 }
 
@@ -331,7 +470,14 @@ hipError_t tiles_of(const TileGrid &g, const LinearParams &p, hipStream_t stream
 
 hipError_t launch_linear_tiles(bool f16, const TileGrid &g, const LinearParams &p, hipStream_t stream)
 {
-    return f16 ? tiles_of<TypeF16, F16Masked>(g, p, stream) : tiles_of<TypeBf16, Bf16Masked>(g, p, stream);
+    return f16 ? tiles_as<TypeF16, F16Masked>(g, p, stream) : tiles_as<TypeBf16, Bf16Masked>(g, p, stream);
+}
+
+hipError_t launch_linear_split(bool f16, const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p,
+                               hipStream_t stream)
+{
+    return f16 ? split_of<TypeF16, F16Masked>(g, splits, steps, parts, p, stream)
+               : split_of<TypeBf16, Bf16Masked>(g, splits, steps, parts, p, stream);
 }
 
 }  // namespace hkg

@@ -27,9 +27,11 @@ struct DropoutCall {
 // x_bits, out_bits: 16 or 32; f16: the 16-bit type is fp16, else bf16
 hipError_t launch_dropout(bool f16, int x_bits, int out_bits, const DropoutCall &p, hipStream_t stream);
 
-// y[M][N] = residual + D(act(A B^T + bias)), A [M][K] and B [N][K] of a 16-bit type.
+// y[M][N] = residual + D(act(A B^T + bias)), A [M][K] and B [N][K] of a 16-bit type; or,
+// transposed, A [K][M] and B [K][N] (tiles only).
 struct LinearParams {
     const uint16_t *A, *B;
+    bool tr_a, tr_b;
     int64_t lda, ldb;
     int M, N, K;
     const void *bias, *residual;   // may be null
@@ -49,19 +51,31 @@ inline LinearParams linear_part(const LinearParams &p, int64_t m, int64_t rows, 
     q.N = (int)cols;
     q.row0 = p.row0 + (int)m;
     q.col0 = p.col0 + (int)n;
-    q.A = p.A + m * p.lda;
-    q.B = p.B + n * p.ldb;
+    q.A = p.A + m * (p.tr_a ? 1 : p.lda);
+    q.B = p.B + n * (p.tr_b ? 1 : p.ldb);
     q.bias = p.bias ? static_cast<const char *>(p.bias) + n * (p.bias_f32 ? 4 : 2) : nullptr;
     q.residual = p.residual ? static_cast<const char *>(p.residual) + (m * p.ldr + n) * e : nullptr;
     q.y = static_cast<char *>(p.y) + (m * p.ldy + n) * e;
     q.z = p.z ? static_cast<char *>(p.z) + (m * p.ldz + n) * 2 : nullptr;
     return q;
 }
-// A grid of Gm x Gn tiles of edge `tile` (256, 192 or 128) and its order (remap.h).
+// A grid of Gm x Gn tiles of edge `tile` (256, 192 or 128; transposed operands: 256 or 128)
+// and its order (remap.h).
 struct TileGrid {
     int tile, Gm, Gn, W, C;
 };
-hipError_t launch_linear_tiles(bool f16, const TileGrid &g, const LinearParams &p, hipStream_t stream);   // K > 0
+// K > 0.  A transposed operand's K is p.K; beside one, an operand that is not has rows of K
+// rounded up to 8 elements, zeros past K.
+hipError_t launch_linear_tiles(bool f16, const TileGrid &g, const LinearParams &p, hipStream_t stream);
+// The same on 128-tiles with K over `splits` workgroups a tile, `steps` K steps of 64 each
+// (the last one the rest, at least one), whose sums go to `parts` (linear_parts_bytes) and
+// are joined, in order, by a second kernel.
+inline int64_t linear_parts_bytes(int64_t M, int64_t N, int64_t splits)
+{
+    return splits * ((M + 127) / 128) * ((N + 127) / 128) * 128 * 128 * 4;
+}
+hipError_t launch_linear_split(bool f16, const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p,
+                               hipStream_t stream);
 hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream);
 
 // What the gradients' products read, formed in one pass (any output may be null):

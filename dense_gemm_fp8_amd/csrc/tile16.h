@@ -30,6 +30,16 @@
 // B's rows are handed to the matrix instruction in the order 32 (j >> 1) + 4 (j & 1)
 // + (x & 3) + 8 (x >> 2), as its first operand, so that a lane's results for two
 // blocks are 8 consecutive columns of one row of C.
+//
+// Transposed operands (kTrA, kTrB; 16-bit types, kT = 256 or 128): an operand may also be
+// held with K along its rows, [K][rows], as the gradients' products meet x, W and dz.  A
+// panel is then 64 rows of K by 2 kT bytes, loaded as it lies, and a fragment is two
+// ds_read_b64_tr_b16: of 16 lanes, lane 4 r + c addresses 4 columns of row r, and lane i
+// receives column i of the four rows.  B's blocks are 16 consecutive columns then.  A
+// row's 16-byte chunks are permuted by an even number, 2 ((k & 3) + 4 (k >> 3 & 1)): the
+// 8 rows x 32 bytes that half a wave reads at once fill the 256-byte bank line.  Every step
+// has a buffer of its own, so that an operand's offsets may pass 32 bits; rows past K read
+// as zeros, being past its range.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -134,6 +144,10 @@ struct TileOperands {
     const void *SA, *SB;         // MXFP4: packed scales and their sizes in bytes
     int sa_bytes, sb_bytes;
 };
+// And where an operand may be transposed.
+struct TransposableOperands : TileOperands {
+    int kt;                      // rows of a transposed operand: K itself, where kb is rounded up
+};
 
 // The scales a wave needs for one K step: [half][word], byte i & 3 of word i >> 2
 // for block i (kB = 8), byte i of word 0 (kB = 4).
@@ -208,8 +222,9 @@ static_assert(plan_ok<8>() && plan_ok<6>() && plan_ok<4>(), "slot plans");
 // Runs the K loop of tile (tm, tn) into acc; smem: 5 panels, nk at least 1 (its first
 // loads, and those of the scales, are not guarded).  On return every load
 // of this wave has landed; other waves may still be reading their last fragments.
-template <class Mma, int kT>
+template <class Mma, int kT, bool kTrA = false, bool kTrB = false>
 struct TileLoop {
+    static_assert((!kTrA && !kTrB) || kT == 256 || kT == 128, "transposed panels");
     static constexpr int kB = kT / 32;
     static constexpr int kPanel = kT * kStepBytes;
     static constexpr int kRingB = 2 * kPanel;
@@ -229,12 +244,51 @@ struct TileLoop {
     int cb_a, cb_b;                // byte of that chunk in a K step
     int pitch_a, pitch_b, kb;
     int la[2], lb[2];              // lane's fragment offset, per half
+    int voff_ta[2], voff_tb[2];    // transposed: lane's load offset for even and odd v
+    int ta[kB], tb[kB];            // and its fragment offset for each block
     int s_off_a, s_off_b, s_last;  // lane's scale byte; offset of the last 128-k step's scales
 
     __device__ __forceinline__ static constexpr int blk_a(int i) { return 16 * i * kStepBytes; }
     __device__ __forceinline__ static constexpr int blk_b(int j) { return (32 * (j >> 1) + 4 * (j & 1)) * kStepBytes; }
 
-    __device__ __forceinline__ void init(const TileOperands &p, char *lds, int tm, int tn)
+    // Transposed panels: rows of 2 kT bytes, kChunks 16-byte chunks; a wave-wide load is
+    // kLoadK rows, and the waves' loads v are 4 kLoadK rows apart.
+    static constexpr int kRowT = 2 * kT, kChunks = kRowT / 16, kLoadK = kLoadBytes / kRowT;
+    __device__ __forceinline__ static int swz_t(int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); }
+    // buffer_of()'s words.
+    __device__ __forceinline__ static i32x4_t resource(const char *base, uint32_t bytes)
+    {
+        const uint64_t at = reinterpret_cast<uint64_t>(base);
+        return i32x4_t{(int)(uint32_t)at, (int)(uint32_t)(at >> 32), (int)bytes, 0x00020000};
+    }
+    // A transposed operand's columns of this tile (`rows` of the product's rows or columns).
+    struct Columns {
+        const char *base;
+        int pitch, width, kt;                    // width: bytes, whole 16-byte chunks
+        // The buffer of K step t.
+        __device__ __forceinline__ i32x4_t step(int t) const
+        {
+            const int left = min(kt - 64 * t, 64);
+            return resource(base + (int64_t)t * 64 * pitch, left > 0 ? panel_range(left, pitch, width) : 0u);
+        }
+    };
+    Columns cols_a, cols_b;
+    i32x4_t plain_a;                             // ra, beside a transposed B
+    __device__ __forceinline__ Columns init_t(const void *base, int pitch, int rows, int kt, int tile, int half,
+                                              int (&voff)[2], int (&t)[kB]) const
+    {
+        const int k = kLoadK * wave + lane / kChunks;
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd)   // rows 4 kLoadK apart: of 256-tiles bit 3 of k follows v
+            voff[odd] = k * pitch + 16 * ((lane % kChunks) ^ swz_t(k + (kT == 256 ? 8 * odd : 0)));
+        const int q = lane >> 4, r = (lane >> 2) & 3, c = lane & 3;
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+            t[j] = (8 * q + r) * kRowT + 16 * (((kChunks / 2 * half + 2 * j) ^ swz_t(8 * q + r)) + (c >> 1)) + 8 * (c & 1);
+        return Columns{static_cast<const char *>(base) + (int64_t)tile * kRowT, pitch, (2 * min(kT, rows - tile * kT) + 15) & ~15, kt};
+    }
+    template <class Operands>
+    __device__ __forceinline__ void init(const Operands &p, char *lds, int tm, int tn)
     {
         smem = lds;
         lane = threadIdx.x & 63;
@@ -245,10 +299,19 @@ struct TileLoop {
         pitch_a = p.pitch_a;
         pitch_b = p.pitch_b;
         kb = p.kb;
-        ra = buffer_of(static_cast<const char *>(p.A) + (int64_t)tm * kT * pitch_a,
-                       panel_range(min(kT, p.rows_a - tm * kT), pitch_a, kb));
-        rb = buffer_of(static_cast<const char *>(p.B) + (int64_t)tn * kT * pitch_b,
-                       panel_range(min(kT, p.rows_b - tn * kT), pitch_b, kb));
+        if constexpr (kTrA)
+            cols_a = init_t(p.A, pitch_a, p.rows_a, p.kt, tm, wave >> 1, voff_ta, ta);
+        else
+            ra = buffer_of(static_cast<const char *>(p.A) + (int64_t)tm * kT * pitch_a,
+                           panel_range(min(kT, p.rows_a - tm * kT), pitch_a, kb));
+        if constexpr (kTrB && !kTrA)
+            plain_a = resource(static_cast<const char *>(p.A) + (int64_t)tm * kT * pitch_a,
+                               panel_range(min(kT, p.rows_a - tm * kT), pitch_a, kb));
+        if constexpr (kTrB)
+            cols_b = init_t(p.B, pitch_b, p.rows_b, p.kt, tn, wave & 1, voff_tb, tb);
+        else
+            rb = buffer_of(static_cast<const char *>(p.B) + (int64_t)tn * kT * pitch_b,
+                           panel_range(min(kT, p.rows_b - tn * kT), pitch_b, kb));
         // row groups u = wave + 4 v: row bits 3, 4 are the wave's for all its loads
         const int r8 = lane >> 3;
         cb_a = ((lane & 7) ^ swz_a(r8 | (wave << 3))) << 4;
@@ -285,6 +348,63 @@ struct TileLoop {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rs, (__attribute__((address_space(3))) void *)(smem + lds_off + 4 * v * kLoadBytes), 16, voff,
             soff + 32 * v * pitch, 0, 0);
+    }
+    // Loads beside transposed operands are in assembly, which writes no register: the
+    // compiler else waits for all loads to LDS before each ds_read_b64_tr_b16 (a gradient of
+    // 8192 x 14336 x 4096 2600 us instead of 650), where the loop waits for those that it
+    // needs.  M0, which takes a wait state, is nobody's between instructions that use it:
+    // each sets it for itself.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+    __device__ __forceinline__ void load_asm(const i32x4_t &rs, int lds_off, int v, int voff, int soff) const
+    {
+        const int at = (int)(uintptr_t)(__attribute__((address_space(3))) char *)smem + lds_off + 4 * v * kLoadBytes;
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff),
+                     "s"(rs), "s"(soff)
+                     : "memory", "m0");
+    }
+#pragma clang diagnostic pop
+    // Load v of a panel.  Transposed: loads v are 4 kLoadK rows apart in step t+2's buffer.
+    __device__ __forceinline__ void load_a(int lds_off, int v, int voff, int soff, const i32x4_t &step) const
+    {
+        if constexpr (kTrA)
+            load_asm(step, lds_off, v, voff_ta[v & 1], 4 * kLoadK * v * pitch_a);
+        else if constexpr (kTrB)
+            load_asm(plain_a, lds_off, v, voff, soff + 32 * v * pitch_a);
+        else
+            load8rows(ra, lds_off, v, voff, soff, pitch_a);
+    }
+    __device__ __forceinline__ void load_b(int lds_off, int v, int voff, int soff, const i32x4_t &step) const
+    {
+        if constexpr (kTrB)
+            load_asm(step, lds_off, v, voff_tb[v & 1], 4 * kLoadK * v * pitch_b);
+        else
+            load8rows(rb, lds_off, v, voff, soff, pitch_b);
+    }
+    // The fragment of a block for half h: its place `at` in the panel from `base` on.
+    template <bool kTr>
+    __device__ __forceinline__ u32x4_t fragment(int base, int blk, int at, int h) const
+    {
+        if constexpr (kTr) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(smem + (at + base) + 32 * h * kRowT)));
+            const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(smem + (at + base) + (32 * h + 4) * kRowT)));
+            return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+            return *reinterpret_cast<const u32x4_t *>(smem + blk + base);
+        }
+    }
+    // What the reads of a panel (wave's first row group at `panel` of its ring) start from:
+    // the lane's offset for half h, or for transposed panels the panel itself.
+    template <bool kTr>
+    __device__ __forceinline__ int read_base(const int (&l)[2], int h, int to_rows, int panel) const
+    {
+        if constexpr (kTr)
+            return hold_s(panel - w_load);
+        else
+            return hold_v(l[h] + hold_s(to_rows + panel));
     }
     // Lane offset in a K step that starts `at` bytes into the rows: a chunk past
     // the rows' end reads zeros (kb is whole chunks).
@@ -336,9 +456,9 @@ struct TileLoop {
                 if (Plan::read(r) != n)
                     continue;
                 if (r < kB)
-                    f.b[1 - kH][r] = *reinterpret_cast<const u32x4_t *>(smem + blk_b(r) + bb);
+                    f.b[1 - kH][r] = fragment<kTrB>(bb, blk_b(r), tb[r], 1 - kH);
                 else
-                    f.a[1 - kH][r - kB] = *reinterpret_cast<const u32x4_t *>(smem + blk_a(r - kB) + ba);
+                    f.a[1 - kH][r - kB] = fragment<kTrA>(ba, blk_a(r - kB), ta[r - kB], 1 - kH);
             }
             hook(slot);
             __builtin_amdgcn_sched_barrier(0);
@@ -359,22 +479,22 @@ struct TileLoop {
             const int vb = kMasked ? masked(voff_b, cb_b, s * kStepBytes) : voff_b;
 #pragma unroll
             for (int v = 0; v < kB; ++v)
-                load8rows(ra, w_load + s * kPanel, v, va, s * kStepBytes, pitch_a);
+                load_a(w_load + s * kPanel, v, va, s * kStepBytes, kTrA ? cols_a.step(s) : i32x4_t{});
 #pragma unroll
             for (int v = 0; v < kB; ++v)
-                load8rows(rb, w_load + kRingB + s * kPanel, v, vb, s * kStepBytes, pitch_b);
+                load_b(w_load + kRingB + s * kPanel, v, vb, s * kStepBytes, kTrB ? cols_b.step(s) : i32x4_t{});
         }
         wait_loads<2 * kB>();
         barrier();
         Frags f;
         {
-            const int ba = hold_v(la[0] + a_rows), bb = hold_v(lb[0] + kRingB + b_rows);
+            const int ba = kTrA ? 0 : hold_v(la[0] + a_rows), bb = kTrB ? kRingB : hold_v(lb[0] + kRingB + b_rows);
 #pragma unroll
             for (int j = 0; j < kB; ++j)
-                f.b[0][j] = *reinterpret_cast<const u32x4_t *>(smem + blk_b(j) + bb);
+                f.b[0][j] = fragment<kTrB>(bb, blk_b(j), tb[j], 0);
 #pragma unroll
             for (int i = 0; i < kB; ++i)
-                f.a[0][i] = *reinterpret_cast<const u32x4_t *>(smem + blk_a(i) + ba);
+                f.a[0][i] = fragment<kTrA>(ba, blk_a(i), ta[i], 0);
         }
         // Nothing is on its way from LDS when the loop begins: the compiler, which orders
         // the reads above as it likes, else waits at the loop's head for every read in
@@ -389,18 +509,22 @@ struct TileLoop {
         int so = 2 * kStepBytes;
         int s_next = 2 * kMxStepScales;              // scales of step t+1
         int vb = kMasked ? masked(voff_b, cb_b, so) : voff_b;
-        int ba0 = hold_v(la[1] + fa + pa), bb0 = hold_v(lb[1] + fb + pb);   // half 1 of step t
+        int ba0 = kTrA ? pa - w_load : hold_v(la[1] + fa + pa), bb0 = kTrB ? pb - w_load : hold_v(lb[1] + fb + pb);   // half 1 of step t
         for (int t = 0; t < nk; ++t) {
             StepScales<kB> next = {};
             int va = voff_a, vb_next = voff_b, ba1 = 0, bb1 = 0;
             int npa = 0, npa1 = 0, nso = 0, npb = 0, npb1 = 0, npb2 = 0;
+            i32x4_t na = {}, nb = {};                    // transposed: step t+2's buffers
+            if constexpr (kTrB)
+                nb = cols_b.step(t + 2);
             __builtin_amdgcn_sched_barrier(0);
             half<0>(
                 f, acc, sc, ba0, bb0,
                 [&](int v) {
                     pb2 = hold_s(pb2);
-                    so = hold_s(so);
-                    load8rows(rb, pb2, v, vb, so, pitch_b);
+                    if constexpr (!kTrB)
+                        so = hold_s(so);
+                    load_b(pb2, v, vb, so, nb);
                 },
                 [&](auto slot) __attribute__((always_inline)) {
                     constexpr int n = decltype(slot)::value;
@@ -411,13 +535,15 @@ struct TileLoop {
                     }
                     if constexpr (n == Plan::kBaseA) {
                         pa1 = hold_s(pa1);
-                        ba1 = hold_v(la[0] + hold_s(fa + pa1));
+                        ba1 = read_base<kTrA>(la, 0, fa, pa1);
                     }
                     if constexpr (n == Plan::kBaseB) {
                         pb1 = hold_s(pb1);
-                        bb1 = hold_v(lb[0] + hold_s(fb + pb1));
+                        bb1 = read_base<kTrB>(lb, 0, fb, pb1);
                     }
-                    if constexpr (kMasked && n == Plan::kMask) {
+                    if constexpr (kTrA && n == Plan::kMask)
+                        na = cols_a.step(t + 2);
+                    if constexpr (kMasked && !kTrA && n == Plan::kMask) {
                         so = hold_s(so);
                         va = hold_v(masked(voff_a, cb_a, so));
                     }
@@ -429,18 +555,19 @@ struct TileLoop {
                 f, acc, sc, ba1, bb1,
                 [&](int v) {
                     pa = hold_s(pa);
-                    so = hold_s(so);
-                    load8rows(ra, pa, v, va, so, pitch_a);
+                    if constexpr (!kTrA)
+                        so = hold_s(so);
+                    load_a(pa, v, va, so, na);
                 },
                 [&](auto slot) __attribute__((always_inline)) {
                     constexpr int n = decltype(slot)::value;
                     if constexpr (n == Plan::kBaseA) {
                         pa1 = hold_s(pa1);
-                        ba0 = hold_v(la[1] + hold_s(fa + pa1));
+                        ba0 = read_base<kTrA>(la, 1, fa, pa1);
                     }
                     if constexpr (n == Plan::kBaseB) {
                         pb1 = hold_s(pb1);
-                        bb0 = hold_v(lb[1] + hold_s(fb + pb1));
+                        bb0 = read_base<kTrB>(lb, 1, fb, pb1);
                     }
                     // the next step's scales move over those no instruction needs any
                     // more (half 0's, and half 1's of A blocks 0..3 after 32 of 64):
@@ -462,7 +589,7 @@ struct TileLoop {
                         npb1 = copy_s(pb2);
                     if constexpr (n == Plan::kRing + 2)
                         npb2 = copy_s(pb);
-                    if constexpr (kMasked && n == Plan::kMask) {
+                    if constexpr (kMasked && !kTrB && n == Plan::kMask) {
                         so = hold_s(so);
                         vb_next = hold_v(masked(voff_b, cb_b, hold_s(so + kStepBytes)));
                     }
