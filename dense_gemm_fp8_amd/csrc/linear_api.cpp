@@ -59,17 +59,31 @@ struct How {
     enum Kind { kFewRows, kSplit, kTiles } kind;
     int splits, steps;
 };
-// `transposed`: the operands may have K along their rows (gradients), which only tiles take.
+// The cheapest by what each takes in ns, fitted to replayed graphs over weights in turn (M
+// 17 .. 1024; N, K 1024 .. 14336), which they meet within a third:
+//   few rows  2000 + rows_grid's a step, for each 256 workgroups; 4000 more where its
+//             operands have to be transposed first
+//   split     8500 + 750 a step of a part; a part for each compute unit, of 8 steps at least
+//   tiles     3000 + 600 a step, for each 256 tiles of 128
+// in us: 32 x 4096 x 4096 10.3, 15.1 (8 parts), 34.3; 256 x 4096 x 4096 29.0, 21.3 (4), 37.2;
+// 100 x 4096 x 14336 42.9, 32.4 (8), 135; 512 x 1024 x 1024 5.6, 10.5 (2), 9.8; 1024 x 1024 x
+// 8192 37.4, 29.9 (4), 56.5; 32 x 8192 x 8192 34.6, 39.2 (4), 71.3; 256 x 14336 x 4096 115, -,
+// 45.5.
 How how_to(int64_t M, int64_t N, int64_t K, bool transposed)
 {
-    const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), steps = ceil_div(K, 64);
-    if (K == 0 || (!transposed && M <= 16) || ceil_div(M, 64) * ceil_div(N, 32) <= 512)
+    if (M == 0 || N == 0 || K == 0 || (!transposed && M <= 16))
         return {How::kFewRows, 0, 0};
-    if (tiles <= 256 && steps >= 16) {
-        const int64_t splits = 512 / tiles < steps / 8 ? 512 / tiles : steps / 8, each = ceil_div(steps, splits);
-        return {How::kSplit, static_cast<int>(ceil_div(steps, each)), static_cast<int>(each)};
+    const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), steps = ceil_div(K, 64);
+    const hkg::RowsGrid rows = hkg::rows_grid(M, N);
+    const int64_t few = (transposed ? 6000 : 2000) + rows.step_ns * steps * ceil_div(rows.blocks(M, N), 256);
+    const int64_t whole = 3000 + 600 * steps * ceil_div(tiles, 256);
+    const int64_t most = steps / 8 < 256 / tiles ? steps / 8 : 256 / tiles;
+    if (most >= 2) {
+        const int64_t each = ceil_div(steps, most), split = 8500 + 750 * each;
+        if (split < few && split < whole)
+            return {How::kSplit, static_cast<int>(ceil_div(steps, each)), static_cast<int>(each)};
     }
-    return {How::kTiles, 0, 0};
+    return {few < whole ? How::kFewRows : How::kTiles, 0, 0};
 }
 int64_t parts_bytes(const How &h, int64_t M, int64_t N)
 {

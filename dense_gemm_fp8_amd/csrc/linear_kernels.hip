@@ -179,42 +179,45 @@ __device__ __forceinline__ f32x4_t mma16(const u32x4_t &a, const u32x4_t &b, con
     }
 }
 
-template <int kMb, int kS>
+// 16 kMb rows x 16 kNb columns, runs of kS steps.
+template <int kMb, int kNb, int kS>
 struct RowsPlan {
     static constexpr int kRow = 64 * kS;                    // bytes of a row in a run
     static constexpr int kChunks = 4 * kS;
-    static constexpr int kB = 32 * kRow, kA = 16 * kMb * kRow;
+    static constexpr int kB = 16 * kNb * kRow, kA = 16 * kMb * kRow;
     static constexpr int kWave = kA + kB;                   // LDS bytes of one wave
-    static constexpr int kSums = kRowWaves * 64 * 9 * 4;
+    static constexpr int kSums = kRowWaves * 64 * (4 * kNb + 1) * 4;
     static constexpr int kLds = kRowWaves * kWave > kSums ? kRowWaves * kWave : kSums;
-    // Places of a row's chunks in LDS, permuted so that the 16 rows of a fragment (B's
-    // differ in bits 0, 1 and 3, 4, A's in 0..3) fall into different 16-byte slots of
-    // the 256-byte bank line.
+    // B's row for lane x of block h: of two blocks interleaved, so that a lane's results
+    // are 8 consecutive columns.
+    __device__ __forceinline__ static int b_row(int x, int h) { return kNb == 1 ? x : (x & 3) + 8 * (x >> 2) + 4 * h; }
+    // Places of a row's chunks in LDS, permuted so that the 16 rows of a fragment fall into
+    // different 16-byte slots of the 256-byte bank line: by the four bits of the row that
+    // vary among them, of which those that the row's own place does not tell apart.
+    __device__ __forceinline__ static int chunk(int bits, int c) { return kS == 4 ? c ^ bits : c ^ (bits >> 1); }
+    __device__ __forceinline__ static int a_chunk(int row, int c) { return chunk(row & 15, c); }
     __device__ __forceinline__ static int b_chunk(int row, int c)
     {
-        return kS == 2 ? c ^ (((row >> 1) & 1) | (((row >> 3) & 3) << 1)) : c ^ ((row >> 3) & 3);
-    }
-    __device__ __forceinline__ static int a_chunk(int row, int c)
-    {
-        return kS == 2 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3);
+        return chunk(kNb == 1 ? row & 15 : (row & 3) | (row >> 3 & 3) << 2, c);
     }
 };
 
-template <class T, int kMb, int kS>
+template <class T, int kMb, int kNb, int kS>
 __global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const LinearParams p)
 {
-    using G = RowsPlan<kMb, kS>;
+    using G = RowsPlan<kMb, kNb, kS>;
+    constexpr int kCols = 16 * kNb;
     __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, q = lane >> 4;
-    const int gn = (p.N + 31) / 32;
-    const int n0 = 32 * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
+    const int gn = (p.N + kCols - 1) / kCols;
+    const int n0 = kCols * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
     const int kb = 2 * p.K, pitch_a = (int)(2 * p.lda), pitch_b = (int)(2 * p.ldb);
     const int rows = min(16 * kMb, p.M - m0);
     char *const lb = smem + wave * G::kWave, *const la = lb + G::kB;
     // buffers over the workgroup's rows: rows past the matrix read zeros
     const __amdgpu_buffer_rsrc_t ra = buffer_of(reinterpret_cast<const char *>(p.A) + (int64_t)m0 * pitch_a, panel_range(rows, pitch_a, kb));
-    const __amdgpu_buffer_rsrc_t rb = buffer_of(reinterpret_cast<const char *>(p.B) + (int64_t)n0 * pitch_b, panel_range(min(32, p.N - n0), pitch_b, kb));
+    const __amdgpu_buffer_rsrc_t rb = buffer_of(reinterpret_cast<const char *>(p.B) + (int64_t)n0 * pitch_b, panel_range(min(kCols, p.N - n0), pitch_b, kb));
     auto to_lds = [&](__amdgpu_buffer_rsrc_t rs, char *to, int voff) __attribute__((always_inline)) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)to, 16, voff, 0, 0, 0);
     };
@@ -232,22 +235,23 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const L
                 to_lds(ra, la + 1024 * d, at < kb ? row * pitch_a + at : kPastEnd);
         }
     };
-    f32x4_t acc[kMb][2];
+    f32x4_t acc[kMb][kNb];
 #pragma unroll
     for (int i = 0; i < kMb; ++i)
-        acc[i][0] = acc[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < kNb; ++h)
+            acc[i][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     const int runs = (kb + G::kRow - 1) / G::kRow;
     if (wave < runs)
         send(wave);
-    const int br = (x & 3) + 8 * (x >> 2);
     for (int r = wave; r < runs; r += kRowWaves) {
-        u32x4_t b[kS][2], a[kS][kMb];
+        u32x4_t b[kS][kNb], a[kS][kMb];
         wait_loads<0>();
 #pragma unroll
         for (int u = 0; u < kS; ++u) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                b[u][h] = *reinterpret_cast<const u32x4_t *>(lb + G::kRow * (br + 4 * h) + 16 * G::b_chunk(br + 4 * h, 4 * u + q));
+            for (int h = 0; h < kNb; ++h)
+                b[u][h] = *reinterpret_cast<const u32x4_t *>(lb + G::kRow * G::b_row(x, h) + 16 * G::b_chunk(G::b_row(x, h), 4 * u + q));
 #pragma unroll
             for (int i = 0; i < kMb; ++i)
                 a[u][i] = *reinterpret_cast<const u32x4_t *>(la + G::kRow * (16 * i + x) + 16 * G::a_chunk(x, 4 * u + q));
@@ -260,29 +264,34 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const L
 #pragma unroll
             for (int i = 0; i < kMb; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < kNb; ++h)
                     acc[i][h] = mma16<T>(b[u][h], a[u][i], acc[i][h]);
     }
     const Key key(p.drop);
-    float(*part)[64][9] = reinterpret_cast<float(*)[64][9]>(smem);   // 9: neighbours' rows fall into other banks
+    constexpr int kPer = 4 * kNb;                            // columns of a lane's results
+    float(*part)[64][kPer + 1] = reinterpret_cast<float(*)[64][kPer + 1]>(smem);   // + 1: neighbours' rows fall into other banks
 #pragma unroll
     for (int i = 0; i < kMb; ++i) {
         // the sums are complete here for every lane: nothing below may move a
         // matrix instruction under a lane mask
-        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]));
+#pragma unroll
+        for (int h = 0; h < kNb; ++h)
+            asm volatile("" : "+v"(acc[i][h]));
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            part[wave][lane][e] = acc[i][0][e];
-            part[wave][lane][4 + e] = acc[i][1][e];
-        }
+        for (int h = 0; h < kNb; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[wave][lane][4 * h + e] = acc[i][h][e];
         __syncthreads();
-        // 16 x 32 results, one a thread: lane 16 (c / 8) + r of the fragments holds row r, column c
-        const int r = threadIdx.x >> 5, c = threadIdx.x & 31, row = m0 + 16 * i + r, col = n0 + c;
+        // 16 x 16 kNb results, one a thread: lane 16 (c / kPer) + r of the fragments holds row r, column c
+        const int r = threadIdx.x / kCols, c = threadIdx.x % kCols, row = m0 + 16 * i + r, col = n0 + c;
+        if (r >= 16)
+            continue;                                        // 16 columns: half of the threads
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWaves; ++w)
-            v += part[w][16 * (c >> 3) + r][c & 7];
+            v += part[w][16 * (c / kPer) + r][c % kPer];
         if (row >= p.M || col >= p.N)
             continue;
         if (p.bias)
@@ -407,21 +416,23 @@ __global__ __launch_bounds__(256) void linear_bias_sum_kernel(const float *sums,
     }
 }
 
-template <class T, int kMb, int kS>
-hipError_t few_rows(const LinearParams &p, unsigned blocks, hipStream_t stream)
+template <class T, int kMb, int kNb, int kS>
+hipError_t few_rows(const LinearParams &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((linear_few_rows_kernel<T, kMb, kS>), dim3(blocks), dim3(64 * kRowWaves), 0, stream, p);
+    const unsigned blocks = (unsigned)((p.N + 16 * kNb - 1) / (16 * kNb)) * (unsigned)((p.M + 16 * kMb - 1) / (16 * kMb));
+    hipLaunchKernelGGL((linear_few_rows_kernel<T, kMb, kNb, kS>), dim3(blocks), dim3(64 * kRowWaves), 0, stream, p);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t few_rows_of(const LinearParams &p, hipStream_t stream)
 {
-    const int mb = p.M > 16 ? 4 : 1;
-    const unsigned blocks = (unsigned)((p.N + 31) / 32) * (unsigned)((p.M + 16 * mb - 1) / (16 * mb));
-    if (mb == 1)
-        return few_rows<T, 1, 2>(p, blocks, stream);
-    return few_rows<T, 4, 2>(p, blocks, stream);
+    const RowsGrid g = rows_grid(p.M, p.N);
+    if (g.mb == 1)
+        return few_rows<T, 1, 1, 4>(p, stream);
+    if (g.mb == 2)
+        return g.nb == 1 ? few_rows<T, 2, 1, 2>(p, stream) : few_rows<T, 2, 2, 2>(p, stream);
+    return g.nb == 1 ? few_rows<T, 4, 1, 2>(p, stream) : few_rows<T, 4, 2, 2>(p, stream);
 }
 
 // f(grid, shift): shapes a launch whose lanes take `cols` columns of a row each.
@@ -464,8 +475,8 @@ hipError_t launch_dropout(bool f16, int x_bits, int out_bits, const DropoutCall 
 hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream)
 {
     constexpr int64_t kMost = int64_t(1) << 22;
-    const int64_t high = p.M > 16 ? ((int64_t)p.M + 63) / 64 : 1;
-    const int64_t turn_m = high < kMost ? p.M : 64 * kMost, turn_n = 32 * (high < kMost ? kMost / high : 1);
+    const int64_t high = ((int64_t)p.M + 31) / 32;          // a workgroup has 16 columns at least, and 32 rows if there are
+    const int64_t turn_m = high < kMost ? p.M : 32 * kMost, turn_n = 16 * (high < kMost ? kMost / high : 1);
     hipError_t e = hipSuccess;
     for (int64_t m = 0; m < p.M && e == hipSuccess; m += turn_m)
         for (int64_t n = 0; n < p.N && e == hipSuccess; n += turn_n) {

@@ -129,7 +129,10 @@ def test_workspace_sizes():
     assert f(1, 4096, 4096) >= 0 and f(-1, 1, 8) == SHAPE and f(1, 1, 4) == SHAPE and f(1, 1, 1 << 22) == SIZE
     assert f(1 << 31, 1, 8) == SIZE
     assert b(64, 96, 64) > 0 and b(64, -1, 64) == SHAPE and b(64, 64, 1 << 22) == SIZE and b(1 << 22, 64, 64) == SIZE
-    assert b(0, 0, 0) >= 0
+    for m in (0, 1, 3000):
+        for n in (0, 1, 3000):
+            for k in (0, 8, 2048):
+                assert f(m, n, k) >= 0 and b(m, n, k) >= 0
 
 
 def test_python_refusals():
