@@ -99,21 +99,28 @@ hipError_t run_product(bool f16, const How &h, const hkg::LinearParams &p, void 
         const hkg::TileOrder o = order_of(p.M, p.N, 2 * static_cast<int64_t>(p.K), 128);
         return hkg::launch_linear_split(f16, {128, o.Gm, o.Gn, o.W, o.C}, h.splits, h.steps, static_cast<float *>(parts), p, stream);
     }
-    // the launches that the GEMM makes of this shape; operands with K along their rows have
-    // no 192-tiles, as MXFP8 has none
-    Plan pl;
+    // The tile that the GEMM takes for this shape (operands with K along their rows have no
+    // 192-tiles, as MXFP8 has none).  Where 256-tiles end in a partial round of the 256
+    // compute units, and at least a tenth of the whole would idle, the whole rounds' rows or
+    // columns on 256-tiles and the rest on 128-tiles: by columns too, unlike the GEMM (a
+    // gradient of 4096 x 14336, K = 8192, 896 tiles: 786 us in four rounds, 735 so).
     const bool transposed = p.tr_a || p.tr_b;
-    if (plan_gemm(transposed ? hkg::kMx : hkg::kBf16, p.M, p.N, transposed ? 2 * static_cast<int64_t>(p.K) : p.K, nullptr, &pl) != HKG_OK)
-        return hipErrorInvalidValue;
-    hipError_t e = hipSuccess;
-    int64_t row = 0;
-    for (int i = 0; i < pl.launches && e == hipSuccess; ++i) {
-        const hkg::TileGrid g = {static_cast<int>(tile_edge(pl.sched[i])), static_cast<int>(pl.Gm[i]),
-                                 static_cast<int>(pl.Gn[i]), pl.W[i], pl.C[i]};
-        e = hkg::launch_linear_tiles(f16, g, hkg::linear_part(p, row, pl.rows[i], 0, p.N), stream);
-        row += pl.rows[i];
-    }
-    return e;
+    const int64_t edge = tile_edge(default_schedule(transposed ? hkg::kMx : hkg::kBf16, p.M, p.N)), bytes = 2 * static_cast<int64_t>(p.K);
+    const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+    TileSplit cut = {0, false};
+    if (edge == 256 && (256 - tiles % 256) * 10 >= 256 * (tiles / 256 + 1))
+        cut = split_last_round(p.M, p.N);
+    const auto launch = [&](const hkg::LinearParams &q, int tile) {
+        const hkg::TileOrder o = order_of(q.M, q.N, bytes, tile);
+        return hkg::launch_linear_tiles(f16, {tile, o.Gm, o.Gn, o.W, o.C}, q, stream);
+    };
+    if (cut.keep == 0)
+        return launch(p, static_cast<int>(edge));
+    const int64_t m = cut.by_rows ? cut.keep : p.M, n = cut.by_rows ? p.N : cut.keep;
+    const hipError_t e = launch(hkg::linear_part(p, 0, m, 0, n), 256);
+    if (e != hipSuccess)
+        return e;
+    return launch(cut.by_rows ? hkg::linear_part(p, m, p.M - m, 0, p.N) : hkg::linear_part(p, 0, p.M, n, p.N - n), 128);
 }
 
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }

