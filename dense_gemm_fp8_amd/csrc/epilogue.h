@@ -48,76 +48,132 @@ __device__ __forceinline__ void store16(void *p, const u32x4_t &v)
         *static_cast<u32x4_any_t *>(p) = v;
 }
 
-// The first n of the eight elements from p (n < 1: none), the rest zeros.
-template <class T, bool kStream = false>
-__device__ __forceinline__ void load8_16(const void *p, int n, float (&v)[8])
+// The first n < 8 of eight elements, as up to three accesses of 4, 2 and 1 of them, all
+// sent before the first is needed.
+typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_any_t __attribute__((aligned(2)));
+// Eight elements of 16 bits in `a`, or of 32 in `a` and `b`.
+struct Raw8 {
+    u32x4_t a, b;
+};
+__device__ __forceinline__ u32x4_t load_tail16(const void *p, int n)
 {
-    u32x4_t w = {0u, 0u, 0u, 0u};
+    const uint16_t *c = static_cast<const uint16_t *>(p);
+    u32x2_t x = {0u, 0u};
+    uint32_t y = 0u, z = 0u;
+    n = n > 0 ? n : 0;
+    if (n & 4)
+        x = *reinterpret_cast<const u32x2_any_t *>(c);
+    if (n & 2)
+        y = *reinterpret_cast<const u32_any_t *>(c + (n & 4));
+    if (n & 1)
+        z = c[n & 6];
+    return u32x4_t{(n & 4 ? x[0] : y) | (n == 1 ? z : 0u), x[1] | (n == 3 ? z : 0u), (n & 4 ? y : 0u) | (n == 5 ? z : 0u),
+                   n == 7 ? z : 0u};
+}
+__device__ __forceinline__ void store_tail16(void *p, int n, const u32x4_t &w)
+{
+    uint16_t *c = static_cast<uint16_t *>(p);
+    n = n > 0 ? n : 0;
+    if (n & 4)
+        *reinterpret_cast<u32x2_any_t *>(c) = u32x2_t{w[0], w[1]};
+    if (n & 2)
+        *reinterpret_cast<u32_any_t *>(c + (n & 4)) = n & 4 ? w[2] : w[0];
+    if (n & 1)
+        c[n & 6] = (uint16_t)(n == 1 ? w[0] : n == 3 ? w[1] : n == 5 ? w[2] : w[3]);
+}
+__device__ __forceinline__ Raw8 load_tail32(const void *p, int n)
+{
+    const uint32_t *c = static_cast<const uint32_t *>(p);
+    u32x4_t x = {0u, 0u, 0u, 0u};
+    u32x2_t y = {0u, 0u};
+    uint32_t z = 0u;
+    n = n > 0 ? n : 0;
+    if (n & 4)
+        x = *reinterpret_cast<const u32x4_any_t *>(c);
+    if (n & 2)
+        y = *reinterpret_cast<const u32x2_any_t *>(c + (n & 4));
+    if (n & 1)
+        z = c[n & 6];
+    const bool f = n & 4;
+    return Raw8{{f ? x[0] : n == 1 ? z : y[0], f ? x[1] : y[1], f ? x[2] : n == 3 ? z : 0u, x[3]},
+                {f ? (n == 5 ? z : y[0]) : 0u, f ? y[1] : 0u, n == 7 ? z : 0u, 0u}};
+}
+__device__ __forceinline__ void store_tail32(void *p, int n, const Raw8 &w)
+{
+    uint32_t *c = static_cast<uint32_t *>(p);
+    n = n > 0 ? n : 0;
+    if (n & 4)
+        *reinterpret_cast<u32x4_any_t *>(c) = w.a;
+    if (n & 2)
+        *reinterpret_cast<u32x2_any_t *>(c + (n & 4)) = n & 4 ? u32x2_t{w.b[0], w.b[1]} : u32x2_t{w.a[0], w.a[1]};
+    if (n & 1)
+        c[n & 6] = n == 1 ? w.a[0] : n == 3 ? w.a[2] : n == 5 ? w.b[0] : w.b[2];
+}
+
+// The first n of the eight elements from p (n < 1: none), the rest zeros.
+template <bool kStream = false>
+__device__ __forceinline__ Raw8 load_raw8(const void *p, int n, bool f32)
+{
+    Raw8 r = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
     if (n >= 8) {
-        w = load16<kStream>(p);
+        r.a = load16<kStream>(p);
+        if (f32)
+            r.b = load16<kStream>(static_cast<const char *>(p) + 16);
+    } else if (f32) {
+        r = load_tail32(p, n);
     } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < n)
-                w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+        r.a = load_tail16(p, n);
     }
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void unpack16(const u32x4_t &w, float (&v)[8])
+{
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[2 * e] = T::low(w[e]);
         v[2 * e + 1] = T::high(w[e]);
     }
 }
-__device__ __forceinline__ void load8_32(const void *p, int n, float (&v)[8])
+__device__ __forceinline__ void unpack32(const Raw8 &w, float (&v)[8])
 {
-    const uint32_t *f = static_cast<const uint32_t *>(p);
-    u32x4_t a = {0u, 0u, 0u, 0u}, b = a;
-    if (n >= 8) {
-        a = load16(f);
-        b = load16(f + 4);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < n)
-                (e < 4 ? a : b)[e & 3] = f[e];
-    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t x = a[e], y = b[e];   // a bit cast of a vector's element reads element 0
+        const uint32_t x = w.a[e], y = w.b[e];   // a bit cast of a vector's element reads element 0
         v[e] = __builtin_bit_cast(float, x);
         v[4 + e] = __builtin_bit_cast(float, y);
     }
 }
 template <class T, bool kStream = false>
+__device__ __forceinline__ void load8_16(const void *p, int n, float (&v)[8])
+{
+    unpack16<T>(load_raw8<kStream>(p, n, false).a, v);
+}
+__device__ __forceinline__ void load8_32(const void *p, int n, float (&v)[8]) { unpack32(load_raw8(p, n, true), v); }
+template <class T, bool kStream = false>
 __device__ __forceinline__ void store8_16(void *p, int n, const float (&v)[8])
 {
     const u32x4_t w = {T::pack2(v[0], v[1]), T::pack2(v[2], v[3]), T::pack2(v[4], v[5]), T::pack2(v[6], v[7])};
-    if (n >= 8) {
+    if (n >= 8)
         store16<kStream>(p, w);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < n)
-                static_cast<uint16_t *>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
+    else
+        store_tail16(p, n, w);
 }
 template <bool kStream = false>
 __device__ __forceinline__ void store8_32(void *p, int n, const float (&v)[8])
 {
-    float *f = static_cast<float *>(p);
+    Raw8 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        w.a[e] = __builtin_bit_cast(uint32_t, v[e]);
+        w.b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
+    }
     if (n >= 8) {
-        u32x4_t a, b;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            a[e] = __builtin_bit_cast(uint32_t, v[e]);
-            b[e] = __builtin_bit_cast(uint32_t, v[4 + e]);
-        }
-        store16<kStream>(f, a);
-        store16<kStream>(f + 4, b);
+        store16<kStream>(p, w.a);
+        store16<kStream>(static_cast<char *>(p) + 16, w.b);
     } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-            if (e < n)
-                f[e] = v[e];
+        store_tail32(p, n, w);
     }
 }
 __device__ __forceinline__ const char *element_at(const void *p, int64_t at, int bytes)

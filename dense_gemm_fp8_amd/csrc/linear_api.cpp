@@ -58,6 +58,7 @@ bool same_matrix(const void *out, int64_t ldo, const void *in, int64_t ldi) { re
 struct How {
     enum Kind { kFewRows, kSplit, kTiles } kind;
     int splits, steps;
+    int64_t few_over;            // how much longer the kernel for few rows takes, ns
 };
 // The cheapest by what each takes in ns, fitted to replayed graphs over weights in turn (M
 // 17 .. 1024; N, K 1024 .. 14336), which they meet within a third:
@@ -72,7 +73,7 @@ struct How {
 How how_to(int64_t M, int64_t N, int64_t K, bool transposed)
 {
     if (M == 0 || N == 0 || K == 0 || (!transposed && M <= 16))
-        return {How::kFewRows, 0, 0};
+        return {How::kFewRows, 0, 0, 0};
     const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), steps = ceil_div(K, 64);
     const hkg::RowsGrid rows = hkg::rows_grid(M, N);
     const int64_t few = (transposed ? 6000 : 2000) + rows.step_ns * steps * ceil_div(rows.blocks(M, N), 256);
@@ -81,9 +82,9 @@ How how_to(int64_t M, int64_t N, int64_t K, bool transposed)
     if (most >= 2) {
         const int64_t each = ceil_div(steps, most), split = 8500 + 750 * each;
         if (split < few && split < whole)
-            return {How::kSplit, static_cast<int>(ceil_div(steps, each)), static_cast<int>(each)};
+            return {How::kSplit, static_cast<int>(ceil_div(steps, each)), static_cast<int>(each), few - split};
     }
-    return {few < whole ? How::kFewRows : How::kTiles, 0, 0};
+    return {few < whole ? How::kFewRows : How::kTiles, 0, 0, few < whole ? 0 : few - whole};
 }
 int64_t parts_bytes(const How &h, int64_t M, int64_t N)
 {
@@ -135,6 +136,10 @@ struct BackwardLayout {
     {
         x = how_to(M, K, N, true);
         w = how_to(N, K, M, true);
+        // both by the kernel for few rows are one launch, with the bias's sums: worth 5 us of
+        // the host's and the GPU's time (500 x 1000 x 768 in fp16 27.6 us a call in four launches)
+        if (x.few_over + w.few_over < 5000 && x.few_over < 4000 && w.few_over < 4000)
+            x = w = {How::kFewRows, 0, 0, 0};
         // the kernel for few rows takes transposed copies, tiles the matrices themselves
         dz = 0;
         dzt = dz + 2 * M * round8(N);
@@ -404,7 +409,12 @@ int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const voi
         p.act = activation;
         rc = launched(hkg::launch_linear_prepare(f16, p, st));
     }
-    hkg::LinearParams q = {};
+    const int groups = static_cast<int>(ceil_div(M, kSumRows));
+    // one launch for both, also where one of them is not wanted (it has no rows then): the
+    // same blocks, and the same bits
+    const bool pair = have && (want_x || want_w) && at.x.kind == How::kFewRows && at.w.kind == How::kFewRows;
+    const hkg::RowsGrid rows_of_both = hkg::rows_grid(M > N ? M : N, K);   // the larger product's
+    hkg::LinearParams q = {}, qx = {}, qw = {};
     q.drop = {0, 1.0f, 0, 0, nullptr};
     q.N = static_cast<int>(K);
     if (rc == HKG_OK && want_x) {
@@ -417,7 +427,10 @@ int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const voi
         q.K = static_cast<int>(q.tr_b ? N : round8(N));
         q.y = dx;
         q.ldy = lddx;
-        rc = launched(run_product(f16, at.x, q, ws + at.parts, st));
+        if (pair)
+            qx = q;
+        else
+            rc = launched(run_product(f16, at.x, q, ws + at.parts, st));
     }
     if (rc == HKG_OK && want_w) {
         q.tr_a = q.tr_b = at.w.kind != How::kFewRows;
@@ -429,11 +442,16 @@ int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const voi
         q.K = static_cast<int>(q.tr_a ? M : round8(M));
         q.y = dw;
         q.ldy = lddw;
-        rc = launched(run_product(f16, at.w, q, ws + at.parts, st));
+        if (pair)
+            qw = q;
+        else
+            rc = launched(run_product(f16, at.w, q, ws + at.parts, st));
     }
-    if (rc == HKG_OK && want_b)
-        rc = launched(hkg::launch_linear_bias_sum(p.sums, static_cast<int>(ceil_div(M, kSumRows)),
-                                                  static_cast<int>(N), dbias, st));
+    if (rc == HKG_OK && pair)
+        rc = launched(hkg::launch_linear_few_rows2(f16, rows_of_both, qx, qw, p.sums, groups, static_cast<int>(N),
+                                                   want_b ? dbias : nullptr, st));
+    if (rc == HKG_OK && want_b && !pair)
+        rc = launched(hkg::launch_linear_bias_sum(p.sums, groups, static_cast<int>(N), dbias, st));
     return rc;
 }
 

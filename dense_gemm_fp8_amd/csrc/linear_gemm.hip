@@ -16,10 +16,11 @@ namespace hkg {
 namespace {
 
 // A wave's quarter of fp32 results in LDS, kRows rows at a time.
-template <int kB>
+// (kRB blocks of rows, kB of columns)
+template <int kRB, int kB>
 struct F32Stage {
     static constexpr int kSide = 16 * kB, kUnits = 4 * kB;             // 16-byte units of a row
-    static constexpr int kPasses = kB == 4 ? 1 : 2, kBlocks = kB / kPasses, kRows = 16 * kBlocks;
+    static constexpr int kPasses = kRB <= 4 ? 1 : 2, kBlocks = kRB / kPasses, kRows = 16 * kBlocks;
     static constexpr int kBytes = kRows * kSide * 4;
     static constexpr int kLanes = kSide / 8;                           // lanes of a row on the way back
     static constexpr int kTurn = kB == 6 ? 3 : 4;                      // groups of a lane in a turn
@@ -48,34 +49,27 @@ __device__ __forceinline__ void acc_to_lds(int at, const f32x4_t &v)
         asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(at), "v"(v), "n"(kOffset) : "memory");
 }
 
-// Raw residual values of 8 columns, 16 or 32 bits each.
-struct Raw8 {
-    u32x4_t a, b;
-};
-
 // The rows of one matrix that a lane goes through: an address per group, moved on by
 // whole turns.
-template <int kB>
+template <int kRB, int kB>
 struct RowPtr {
-    using St = F32Stage<kB>;
+    using St = F32Stage<kRB, kB>;
     char *at[St::kAligned ? 1 : St::kTurn];
-    int64_t group, turn;                                     // bytes from group to group (aligned), turn to turn
-    __device__ __forceinline__ void init(const void *base, int64_t ld, int bytes, int row, int col, int lane)
+    int64_t row;                                             // bytes from row to row
+    __device__ __forceinline__ void init(const void *base, int64_t ld, int bytes, int row0, int col, int lane)
     {
-        ld *= bytes;
-        turn = St::kTurnRows * ld;
-        group = 64 / St::kLanes * ld;
+        row = ld * bytes;
 #pragma unroll
         for (int u = 0; u < (St::kAligned ? 1 : St::kTurn); ++u)
-            at[u] = static_cast<char *>(const_cast<void *>(base)) + (row + (64 * u + lane) / St::kLanes) * ld +
+            at[u] = static_cast<char *>(const_cast<void *>(base)) + (row0 + (64 * u + lane) / St::kLanes) * row +
                     (int64_t)(col + 8 * ((64 * u + lane) % St::kLanes)) * bytes;
     }
-    __device__ __forceinline__ char *get(int u) const { return St::kAligned ? at[0] + u * group : at[u]; }
+    __device__ __forceinline__ char *get(int u) const { return St::kAligned ? at[0] + u * (64 / St::kLanes) * row : at[u]; }
     __device__ __forceinline__ void next()
     {
 #pragma unroll
         for (int u = 0; u < (St::kAligned ? 1 : St::kTurn); ++u)
-            at[u] += turn;
+            at[u] += St::kTurnRows * row;
     }
 };
 
@@ -87,15 +81,15 @@ struct RowPtr {
 // turns of kTurn groups of 8 columns a lane.  kWhole: the quarter lies inside the matrix.
 // kTrB: B is transposed, whose blocks are 16 consecutive columns, and the product is one of
 // the gradients', whose results go out as they are in 16 bits.
-template <class T, int kB, bool kWhole, bool kTrB>
+template <class T, int kRB, int kB, bool kWhole, bool kTrB>
 struct Epilogue {
-    using St = F32Stage<kB>;
+    using St = F32Stage<kRB, kB>;
     const LinearParams &p;
     char *const mine;
     const int lane, row0, col0;
     int col[St::kTurn];
     float bias[St::kTurn][8];
-    RowPtr<kB> y, z, r;
+    RowPtr<kRB, kB> y, z, r;
     Raw8 next[St::kTurn];
 
     __device__ __forceinline__ int columns(int u) const { return kWhole ? 8 : hold_v(p.N - col[u]); }   // (held: else the
@@ -136,28 +130,8 @@ struct Epilogue {
         if (kTrB || !p.residual || turn >= St::kPasses * St::kTurns)
             return;
 #pragma unroll
-        for (int u = 0; u < St::kTurn; ++u) {
-            const int m = columns(u);
-            const char *const from = r.get(u);
-            Raw8 w = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
-            if (inside(turn, u)) {
-                if (m >= 8) {
-                    w.a = load16(from);
-                    if (p.y_f32)
-                        w.b = load16(from + 16);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (e < m) {
-                            if (p.y_f32)
-                                (e < 4 ? w.a : w.b)[e & 3] = reinterpret_cast<const uint32_t *>(from)[e];
-                            else
-                                w.a[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t *>(from)[e] << (16 * (e & 1));
-                        }
-                }
-            }
-            next[u] = w;
-        }
+        for (int u = 0; u < St::kTurn; ++u)
+            next[u] = load_raw8(r.get(u), inside(turn, u) ? columns(u) : 0, p.y_f32);
         r.next();
     }
     // One turn, whose rows start `local` rows into what LDS holds.
@@ -235,7 +209,7 @@ struct Epilogue {
         }
         y.next();
     }
-    __device__ __forceinline__ void run(f32x4_t (&acc)[kB][kB])
+    __device__ __forceinline__ void run(f32x4_t (&acc)[kRB][kB])
     {
         const Key key(p.drop);
         const int x = lane & 15, q = lane >> 4;
@@ -263,6 +237,18 @@ struct Epilogue {
     }
 };
 
+// The rows from row0 on, columns from col0 on.
+template <class T, bool kTrB, int kRB, int kB>
+__device__ __forceinline__ void finish(const LinearParams &p, char *lds, int lane, int row0, int col0, f32x4_t (&acc)[kRB][kB])
+{
+    if (row0 + 16 * kRB <= p.M && col0 + 16 * kB <= p.N)
+        Epilogue<T, kRB, kB, true, kTrB>(p, lds, lane, row0, col0).run(acc);
+    else
+        Epilogue<T, kRB, kB, false, kTrB>(p, lds, lane, row0, col0).run(acc);
+}
+// The last matrix instructions' results are there, for what reads them in assembly.
+__device__ __forceinline__ void results_ready() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
 template <int kB>
 __device__ __forceinline__ void clear(f32x4_t (&acc)[kB][kB])
 {
@@ -278,7 +264,7 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void linear_tile_kernel(con
 {
     using Loop = TileLoop<Mma, kT, kTrA, kTrB>;
     constexpr int kB = Loop::kB;
-    static_assert(4 * F32Stage<kB>::kBytes <= Loop::kLds, "the stage fits");
+    static_assert(4 * F32Stage<kB, kB>::kBytes <= Loop::kLds, "the stage fits");
     __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
     int tm, tn;
     remap_tile(blockIdx.x, o.Gm, o.Gn, o.W, o.C, tm, tn);
@@ -288,14 +274,81 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void linear_tile_kernel(con
     loop.init(o, smem, tm, tn);
     loop.run(acc, o.nk);
     settle(acc);
-    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");       // the last matrix instructions' results are there
+    results_ready();
     const int row0 = tm * kT + loop.a_rows / kStepBytes, col0 = tn * kT + loop.b_rows / kStepBytes;
-    char *const mine = smem + loop.wave * F32Stage<kB>::kBytes;
     barrier();   // every wave has read its last fragments
-    if (row0 + 16 * kB <= p.M && col0 + 16 * kB <= p.N)
-        Epilogue<T, kB, true, kTrB>(p, mine, loop.lane, row0, col0).run(acc);
-    else
-        Epilogue<T, kB, false, kTrB>(p, mine, loop.lane, row0, col0).run(acc);
+    finish<T, kTrB>(p, smem + loop.wave * F32Stage<kB, kB>::kBytes, loop.lane, row0, col0, acc);
+}
+
+// ---- 128-tiles with K over two groups of waves -------------------------------------------
+// For grids of at most one tile a compute unit: four waves alone wait for their loads most of
+// the time (0.6 us a K step, of which the matrix instructions take 0.25).  Eight waves, each
+// group of four with half of K and a ring of its own; then wave w of group 0 gets the sums of
+// rows 0 .. 31 of its quarter, wave w of group 1 those of rows 32 .. 63.
+template <bool kTrA, bool kTrB>
+__device__ __forceinline__ TransposableOperands part_of(const TransposableOperands &all, int first, int steps)   // of K
+{
+    TransposableOperands o = all;
+    o.A = static_cast<const char *>(o.A) + (int64_t)first * (kTrA ? 64 * (int64_t)o.pitch_a : kStepBytes);
+    o.B = static_cast<const char *>(o.B) + (int64_t)first * (kTrB ? 64 * (int64_t)o.pitch_b : kStepBytes);
+    o.kb = max(min(steps * kStepBytes, all.kb - first * kStepBytes), 0);
+    o.kt = max(min(steps * 64, all.kt - first * 64), 0);
+    return o;
+}
+constexpr int kGroupLds = TileLoop<Bf16Masked, 128>::kLds;
+
+template <class Mma, bool kTrA, bool kTrB>
+struct TwoGroups {
+    using Loop = TileLoop<Mma, 128, kTrA, kTrB>;
+    Loop loop;
+    int group;
+    f32x4_t sum[2][4];
+
+    // K steps k0 .. k0 + steps - 1 (of all.nk) of tile (tm, tn), half of them a group
+    __device__ __forceinline__ void run(const TransposableOperands &all, char *smem, int tm, int tn, int k0, int steps)
+    {
+        group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+        const int each = (steps + 1) / 2, first = k0 + group * each, mine = group == 0 ? each : steps - each;
+        f32x4_t acc[4][4];
+        clear(acc);
+        // both groups go through `each` steps, which share their barriers; past its part a
+        // group's operands are zeros
+        loop.init(part_of<kTrA, kTrB>(all, first, mine), smem + group * kGroupLds, tm, tn, (threadIdx.x >> 6) & 3);
+        loop.run(acc, each);
+        settle(acc);
+        barrier();                                   // every wave has read its last fragments
+        // a wave's other half to its partner: KiB (w, i, j), lane by lane
+        char *const at = smem + loop.lane * 16;
+        const int to = (loop.wave * 2 + (1 - group)) * 8, from = (loop.wave * 2 + group) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<f32x4_t *>(at + (to + 4 * i + j) * 1024) = group == 0 ? acc[2 + i][j] : acc[i][j];
+                sum[i][j] = group == 0 ? acc[i][j] : acc[2 + i][j];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x4_t v = *reinterpret_cast<const f32x4_t *>(at + (from + 4 * i + j) * 1024);
+                sum[i][j] = group == 0 ? sum[i][j] + v : v + sum[i][j];
+            }
+        __syncthreads();                             // the LDS is free again
+    }
+};
+
+template <class T, class Mma, bool kTrA, bool kTrB>
+__global__ __launch_bounds__(512, 1) void linear_tile2_kernel(const TransposableOperands o, const LinearParams p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[2 * kGroupLds];
+    int tm, tn;
+    remap_tile(blockIdx.x, o.Gm, o.Gn, o.W, o.C, tm, tn);
+    TwoGroups<Mma, kTrA, kTrB> g;
+    g.run(o, smem, tm, tn, 0, o.nk);
+    const int row0 = tm * 128 + g.loop.a_rows / kStepBytes + 32 * g.group, col0 = tn * 128 + g.loop.b_rows / kStepBytes;
+    finish<T, kTrB>(p, smem + (4 * g.group + g.loop.wave) * F32Stage<2, 4>::kBytes, g.loop.lane, row0, col0, g.sum);
 }
 
 // ---- K over several workgroups ----------------------------------------------------------
@@ -305,37 +358,42 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void linear_tile_kernel(con
 // those lane 16 q + x's four columns 8 q + 4 (j & 1) .. of row x.
 constexpr int kPartQuarter = 64 * 64;   // floats
 
-template <class Mma, bool kTrA, bool kTrB>
-__global__ __launch_bounds__(256, 2) void linear_part_kernel(const TransposableOperands all, int steps, float *parts)
+template <bool kTrB, int kRB>
+__device__ __forceinline__ void store_part(float *to, int lane, int first, const f32x4_t (&acc)[kRB][4])
 {
-    using Loop = TileLoop<Mma, 128, kTrA, kTrB>;
-    constexpr int kB = Loop::kB;
-    __shared__ __attribute__((aligned(1024))) char smem[Loop::kLds];
-    const int tiles = all.Gm * all.Gn, split = blockIdx.x / tiles, block = blockIdx.x % tiles, k0 = split * steps;
-    TransposableOperands o = all;
-    o.A = static_cast<const char *>(o.A) + (int64_t)k0 * (kTrA ? 64 * (int64_t)o.pitch_a : kStepBytes);
-    o.B = static_cast<const char *>(o.B) + (int64_t)k0 * (kTrB ? 64 * (int64_t)o.pitch_b : kStepBytes);
-    o.nk = min(steps, all.nk - k0);
-    o.kb = min(steps * kStepBytes, all.kb - k0 * kStepBytes);
-    o.kt = min(steps * 64, all.kt - k0 * 64);
-    int tm, tn;
-    remap_tile(block, o.Gm, o.Gn, o.W, o.C, tm, tn);
-    f32x4_t acc[kB][kB];
-    clear(acc);
-    Loop loop;
-    loop.init(o, smem, tm, tn);
-    loop.run(acc, o.nk);
-    settle(acc);
-    float *const to = parts + ((int64_t)split * tiles + (int64_t)tm * o.Gn + tn) * (4 * kPartQuarter) + loop.wave * kPartQuarter;
-    const int x = loop.lane & 15, q = loop.lane >> 4;
+    const int x = lane & 15, q = lane >> 4;
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
+    for (int i = 0; i < kRB; ++i)
 #pragma unroll
-        for (int j = 0; j < kB; ++j) {
+        for (int j = 0; j < 4; ++j) {
             // transposed B: unit 4 j + q of 4 columns instead of 8 (j / 2) + 2 q + j % 2
             const int jj = kTrB ? 2 * (j >> 1) + (q & 1) : j, qq = kTrB ? 2 * (j & 1) + (q >> 1) : q;
-            *reinterpret_cast<f32x4_t *>(to + ((i * kB + jj) * 64 + 16 * qq + x) * 4) = acc[i][j];
+            *reinterpret_cast<f32x4_t *>(to + (((first + i) * 4 + jj) * 64 + 16 * qq + x) * 4) = acc[i][j];
         }
+}
+
+// kTwo: two groups of waves, as above.
+template <class Mma, bool kTrA, bool kTrB, bool kTwo>
+__global__ __launch_bounds__(kTwo ? 512 : 256, kTwo ? 1 : 2) void linear_part_kernel(const TransposableOperands all, int steps, float *parts)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[kTwo ? 2 * kGroupLds : kGroupLds];
+    const int tiles = all.Gm * all.Gn, split = blockIdx.x / tiles, block = blockIdx.x % tiles, k0 = split * steps;
+    int tm, tn;
+    remap_tile(block, all.Gm, all.Gn, all.W, all.C, tm, tn);
+    float *const to = parts + ((int64_t)split * tiles + (int64_t)tm * all.Gn + tn) * (4 * kPartQuarter);
+    if constexpr (kTwo) {
+        TwoGroups<Mma, kTrA, kTrB> g;
+        g.run(all, smem, tm, tn, k0, min(steps, all.nk - k0));
+        store_part<kTrB>(to + g.loop.wave * kPartQuarter, g.loop.lane, 2 * g.group, g.sum);
+    } else {
+        TileLoop<Mma, 128, kTrA, kTrB> loop;
+        f32x4_t acc[4][4];
+        clear(acc);
+        loop.init(part_of<kTrA, kTrB>(all, k0, steps), smem, tm, tn);
+        loop.run(acc, min(steps, all.nk - k0));
+        settle(acc);
+        store_part<kTrB>(to + loop.wave * kPartQuarter, loop.lane, 0, acc);
+    }
 }
 
 // A wave joins one 16 x 32 block: a lane has 8 columns of a row.
@@ -424,6 +482,11 @@ TransposableOperands operands(const TileGrid &g, const LinearParams &p)
     return o;
 }
 
+// K steps from which two groups of waves gain more than their exchange costs: 1111 x 2777 x
+// 1184 (19 steps) 17.1 us against 15.8, 1024 x 4096 x 4096 40.7 against 37.1; a gradient of 1024 x
+// 1024 with K = 64 7.0 against 8.7.
+constexpr int kTwoFrom = 12;
+
 template <class T, class Mma, bool kTrA, bool kTrB>
 hipError_t tiles_of(const TileGrid &g, const LinearParams &p, hipStream_t stream)
 {
@@ -431,6 +494,8 @@ hipError_t tiles_of(const TileGrid &g, const LinearParams &p, hipStream_t stream
     const dim3 grid((unsigned)g.Gm * (unsigned)g.Gn), block(256);
     if (g.tile == 256)
         hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 256, kTrA, kTrB>), grid, block, 0, stream, o, p);
+    else if (g.tile == 128 && g.Gm * g.Gn <= 256 && o.nk >= kTwoFrom)
+        hipLaunchKernelGGL((linear_tile2_kernel<T, Mma, kTrA, kTrB>), grid, dim3(512), 0, stream, o, p);
     else if (g.tile == 128)
         hipLaunchKernelGGL((linear_tile_kernel<T, Mma, 128, kTrA, kTrB>), grid, block, 0, stream, o, p);
     else if constexpr (!kTrA && !kTrB)
@@ -447,22 +512,34 @@ hipError_t tiles_as(const TileGrid &g, const LinearParams &p, hipStream_t stream
                   : tiles_of<T, Mma, false, false>(g, p, stream);
 }
 
+// Parts of many steps by two groups of waves: 128 x 8192 x 8192 in 4 parts of 32 steps 40.4 us
+// against 36.9, 512 x 4096 x 14336 in 2 of 112 82.9 against 76.3; of 8 steps (128 x 4096 x 4096
+// in 8) 16.9 against 18.4.
+template <class Mma, bool kTrA, bool kTrB>
+void part_launch(unsigned blocks, const TransposableOperands &o, int steps, float *parts, hipStream_t stream)
+{
+    if (steps >= (kTrB ? 64 : 32))
+        hipLaunchKernelGGL((linear_part_kernel<Mma, kTrA, kTrB, true>), dim3(blocks), dim3(512), 0, stream, o, steps, parts);
+    else
+        hipLaunchKernelGGL((linear_part_kernel<Mma, kTrA, kTrB, false>), dim3(blocks), dim3(256), 0, stream, o, steps, parts);
+}
+
 template <class T, class Mma>
 hipError_t split_of(const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p, hipStream_t stream)
 {
     const TransposableOperands o = operands(g, p);
     const int tiles = g.Gm * g.Gn;
-    const dim3 grid((unsigned)tiles * (unsigned)splits), block(256);
+    const unsigned blocks = (unsigned)tiles * (unsigned)splits;
     if (p.tr_a)
-        hipLaunchKernelGGL((linear_part_kernel<Mma, true, true>), grid, block, 0, stream, o, steps, parts);
+        part_launch<Mma, true, true>(blocks, o, steps, parts, stream);
     else if (p.tr_b)
-        hipLaunchKernelGGL((linear_part_kernel<Mma, false, true>), grid, block, 0, stream, o, steps, parts);
+        part_launch<Mma, false, true>(blocks, o, steps, parts, stream);
     else
-        hipLaunchKernelGGL((linear_part_kernel<Mma, false, false>), grid, block, 0, stream, o, steps, parts);
+        part_launch<Mma, false, false>(blocks, o, steps, parts, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    hipLaunchKernelGGL(linear_join_kernel<T>, dim3(8u * (unsigned)tiles), block, 0, stream, p, g.Gn, tiles, splits, parts);
+    hipLaunchKernelGGL(linear_join_kernel<T>, dim3(8u * (unsigned)tiles), dim3(256), 0, stream, p, g.Gn, tiles, splits, parts);
     return hipGetLastError();
 }
 

@@ -101,6 +101,11 @@ inline RowsGrid rows_grid(int64_t M, int64_t N)
 }
 hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t stream);
 
+// Two products (either may have M = 0) in blocks of grid `g`, 16 rows as 32, and unless dbias
+// is null launch_linear_bias_sum, in one launch (of at most 2^22 workgroups).
+hipError_t launch_linear_few_rows2(bool f16, const RowsGrid &g, const LinearParams &p, const LinearParams &p2, const float *sums, int groups, int N,
+                                   float *dbias, hipStream_t stream);
+
 // What the gradients' products read, formed in one pass (any output may be null):
 //   dz  [M][Np] and dzt [N][Mp]   dz and its transpose, zeros past N and M
 //   wt  [K][Np], xt [K][Mp]       the transposes of W [N][K] and x [M][K]

@@ -23,16 +23,13 @@ constexpr int kDropRows = 4;
 template <class T, int kBits>
 __device__ __forceinline__ void load4(const void *p, int n, float (&v)[4])
 {
-    typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(2)));
     if constexpr (kBits == 16) {
-        u32x2_t w = {0u, 0u};
+        u32x2_t w;
         if (n >= 4) {
             w = __builtin_nontemporal_load(static_cast<const u32x2_any_t *>(p));
         } else {
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                if (e < n)
-                    w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+            const u32x4_t t = load_tail16(p, n);
+            w = u32x2_t{t[0], t[1]};
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -40,15 +37,7 @@ __device__ __forceinline__ void load4(const void *p, int n, float (&v)[4])
             v[2 * e + 1] = T::high(w[e]);
         }
     } else {
-        u32x4_t w = {0u, 0u, 0u, 0u};
-        if (n >= 4) {
-            w = load16<true>(p);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-                if (e < n)
-                    w[e] = static_cast<const uint32_t *>(p)[e];
-        }
+        const u32x4_t w = n >= 4 ? load16<true>(p) : load_tail32(p, n).a;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t x = w[e];
@@ -58,18 +47,14 @@ __device__ __forceinline__ void load4(const void *p, int n, float (&v)[4])
 }
 __device__ __forceinline__ void store4(float *p, int n, const float (&v)[4])
 {
-    if (n >= 4) {
-        u32x4_t w;
+    Raw8 w = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = __builtin_bit_cast(uint32_t, v[e]);
-        store16<true>(p, w);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (e < n)
-                p[e] = v[e];
-    }
+    for (int e = 0; e < 4; ++e)
+        w.a[e] = __builtin_bit_cast(uint32_t, v[e]);
+    if (n >= 4)
+        store16<true>(p, w.a);
+    else
+        store_tail32(p, n, w);
 }
 
 // Results of 16 bits: a lane's 8 columns are one call of the generator.
@@ -203,15 +188,14 @@ struct RowsPlan {
 };
 
 template <class T, int kMb, int kNb, int kS>
-__global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const LinearParams p)
+__device__ __forceinline__ void few_rows_block(const LinearParams &p, int block, char *smem)
 {
     using G = RowsPlan<kMb, kNb, kS>;
     constexpr int kCols = 16 * kNb;
-    __shared__ __attribute__((aligned(1024))) char smem[G::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int x = lane & 15, q = lane >> 4;
     const int gn = (p.N + kCols - 1) / kCols;
-    const int n0 = kCols * (blockIdx.x % gn), m0 = 16 * kMb * (blockIdx.x / gn);
+    const int n0 = kCols * (block % gn), m0 = 16 * kMb * (block / gn);
     const int kb = 2 * p.K, pitch_a = (int)(2 * p.lda), pitch_b = (int)(2 * p.ldb);
     const int rows = min(16 * kMb, p.M - m0);
     char *const lb = smem + wave * G::kWave, *const la = lb + G::kB;
@@ -314,6 +298,66 @@ __global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const L
     }
 }
 
+template <class T, int kMb, int kNb, int kS>
+__global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_kernel(const LinearParams p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[RowsPlan<kMb, kNb, kS>::kLds];
+    few_rows_block<T, kMb, kNb, kS>(p, blockIdx.x, smem);
+}
+
+// dbias: 16 columns a workgroup, kTall rows of sums at a time, four of them in flight: 128 x
+// 14336 in 3 us (with 32 columns, 8 rows and one in flight 9).
+struct BiasSum {
+    const float *sums;
+    int groups, N;
+    float *dbias;
+};
+template <int kTall>
+__device__ __forceinline__ void bias_sum_block(const BiasSum &b, int block, char *smem)
+{
+    float(*part)[16] = reinterpret_cast<float(*)[16]>(smem);
+    const int c = threadIdx.x & 15, w = threadIdx.x >> 4, col = 16 * block + c;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = w; g < b.groups; g += 4 * kTall)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            s[k] += g + kTall * k < b.groups && col < b.N ? b.sums[(int64_t)(g + kTall * k) * b.N + col] : 0.f;
+    part[w][c] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    if (w == 0 && col < b.N) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kTall; ++i)
+            t += part[i][c];
+        b.dbias[col] = t;
+    }
+}
+__global__ __launch_bounds__(256) void linear_bias_sum_kernel(const BiasSum b)
+{
+    __shared__ char smem[16 * 16 * 4];
+    bias_sum_block<16>(b, blockIdx.x, smem);
+}
+
+// Both gradients of a small layer and its bias's: the first `first` workgroups are the first
+// product's, those up to `second` the other's, the rest sum.
+struct FewRowsPair {
+    LinearParams p[2];
+    int first, second;
+    BiasSum bias;
+};
+template <class T, int kMb, int kNb, int kS>
+__global__ __launch_bounds__(64 * kRowWaves) void linear_few_rows_pair_kernel(const FewRowsPair t)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[RowsPlan<kMb, kNb, kS>::kLds];
+    const int block = blockIdx.x;
+    if (block >= t.second)
+        bias_sum_block<32>(t.bias, block - t.second, smem);
+    else if (block >= t.first)
+        few_rows_block<T, kMb, kNb, kS>(t.p[1], block - t.first, smem);
+    else
+        few_rows_block<T, kMb, kNb, kS>(t.p[0], block, smem);
+}
+
 // ---- what the gradients' products read ------------------------------------------------
 // 64 x 64 tiles through LDS: a tile of dz, of W or of x a workgroup.  A lane reads 8
 // elements of a row, and for the transpose gathers 8 of a column from LDS, whose rows
@@ -397,28 +441,6 @@ __global__ __launch_bounds__(256) void linear_prepare_kernel(const PrepareParams
     }
 }
 
-// 16 columns a workgroup, 16 rows of sums at a time, four of them in flight: 128 x 14336 in
-// 3 us (with 32 columns, 8 rows and one in flight 9).
-__global__ __launch_bounds__(256) void linear_bias_sum_kernel(const float *sums, int groups, int N, float *dbias)
-{
-    __shared__ float part[16][16];
-    const int c = threadIdx.x & 15, w = threadIdx.x >> 4, col = 16 * blockIdx.x + c;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int g = w; g < groups; g += 64)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            s[k] += g + 16 * k < groups && col < N ? sums[(int64_t)(g + 16 * k) * N + col] : 0.f;
-    part[w][c] = (s[0] + s[1]) + (s[2] + s[3]);
-    __syncthreads();
-    if (w == 0 && col < N) {
-        float t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            t += part[i][c];
-        dbias[col] = t;
-    }
-}
-
 template <class T, int kMb, int kNb, int kS>
 hipError_t few_rows(const LinearParams &p, hipStream_t stream)
 {
@@ -436,6 +458,23 @@ hipError_t few_rows_of(const LinearParams &p, hipStream_t stream)
     if (g.mb == 2)
         return g.nb == 1 ? few_rows<T, 2, 1, 2>(p, stream) : few_rows<T, 2, 2, 2>(p, stream);
     return g.nb == 1 ? few_rows<T, 4, 1, 2>(p, stream) : few_rows<T, 4, 2, 2>(p, stream);
+}
+
+template <class T, int kMb, int kNb, int kS>
+hipError_t few_rows_pair(FewRowsPair &t, const RowsGrid &g, hipStream_t stream)
+{
+    t.first = (int)g.blocks(t.p[0].M, t.p[0].N);
+    t.second = t.first + (int)g.blocks(t.p[1].M, t.p[1].N);
+    const int blocks = t.second + (t.bias.dbias ? (t.bias.N + 15) / 16 : 0);
+    hipLaunchKernelGGL((linear_few_rows_pair_kernel<T, kMb, kNb, kS>), dim3((unsigned)blocks), dim3(64 * kRowWaves), 0, stream, t);
+    return hipGetLastError();
+}
+template <class T>
+hipError_t few_rows_pair_of(const RowsGrid &g, FewRowsPair &t, hipStream_t stream)
+{
+    if (g.mb <= 2)
+        return few_rows_pair<T, 2, 1, 2>(t, RowsGrid{2, 1, 2, 0}, stream);
+    return g.nb == 1 ? few_rows_pair<T, 4, 1, 2>(t, g, stream) : few_rows_pair<T, 4, 2, 2>(t, g, stream);
 }
 
 // f(grid, shift): shapes a launch whose lanes take `cols` columns of a row each.
@@ -489,6 +528,13 @@ hipError_t launch_linear_few_rows(bool f16, const LinearParams &p, hipStream_t s
     return e;
 }
 
+hipError_t launch_linear_few_rows2(bool f16, const RowsGrid &g, const LinearParams &p, const LinearParams &p2, const float *sums, int groups, int N,
+                                   float *dbias, hipStream_t stream)
+{
+    FewRowsPair t = {{p, p2}, 0, 0, {sums, groups, N, dbias}};
+    return f16 ? few_rows_pair_of<TypeF16>(g, t, stream) : few_rows_pair_of<TypeBf16>(g, t, stream);
+}
+
 hipError_t launch_linear_prepare(bool f16, const PrepareParams &p, hipStream_t stream)
 {
     const auto tiles = [](int64_t r, int64_t c) { return (r + kPrep - 1) / kPrep * ((c + kPrep - 1) / kPrep); };
@@ -505,7 +551,7 @@ hipError_t launch_linear_prepare(bool f16, const PrepareParams &p, hipStream_t s
 
 hipError_t launch_linear_bias_sum(const float *sums, int groups, int N, float *dbias, hipStream_t stream)
 {
-    hipLaunchKernelGGL(linear_bias_sum_kernel, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, sums, groups, N, dbias);
+    hipLaunchKernelGGL(linear_bias_sum_kernel, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, BiasSum{sums, groups, N, dbias});
     return hipGetLastError();
 }
 

@@ -288,11 +288,11 @@ struct TileLoop {
         return Columns{static_cast<const char *>(base) + (int64_t)tile * kRowT, pitch, (2 * min(kT, rows - tile * kT) + 15) & ~15, kt};
     }
     template <class Operands>
-    __device__ __forceinline__ void init(const Operands &p, char *lds, int tm, int tn)
+    __device__ __forceinline__ void init(const Operands &p, char *lds, int tm, int tn, int of = threadIdx.x >> 6)
     {
         smem = lds;
         lane = threadIdx.x & 63;
-        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wave = __builtin_amdgcn_readfirstlane(of);   // of the four that share the tile
         w_load = wave * kLoadBytes;
         a_rows = (kT / 2) * (wave >> 1) * kStepBytes;
         b_rows = (kT / 2) * (wave & 1) * kStepBytes;
