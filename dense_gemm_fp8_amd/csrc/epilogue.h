@@ -248,8 +248,9 @@ constexpr float kTanhC = 2.0f * 0.79788456f * kLog2e;   // 2 sqrt(2 / pi), for p
 constexpr float kTanhA = 0.044715f;
 constexpr float kLargest = 3.4e38f;
 
-// z, with -infinity replaced by a number: 0 times it is then 0.  A NaN stays one.
-__device__ __forceinline__ float above_minus_inf(float z) { return z < -kLargest ? -kLargest : z; }
+// z times a share s(z) of it that is 0 at -infinity: the product is 0 there too.  A NaN
+// comes through s.
+__device__ __forceinline__ float share(float z, float s) { return __builtin_fmaxf(z, -kLargest) * s; }
 
 // 1 / (1 + 2^-u): 2^-u may be infinity, which gives 0.
 __device__ __forceinline__ float sigmoid2(float u) { return rcp_of(1.0f + exp2_of(-u)); }
@@ -281,18 +282,12 @@ __device__ __forceinline__ float act_of(float z)
 {
     if constexpr (kAct == kActRelu)
         return z <= 0.0f ? 0.0f : z;
-    if constexpr (kAct == kActGelu) {
-        const float c = above_minus_inf(z);
-        return c * Normal(c).phi;
-    }
-    if constexpr (kAct == kActGeluTanh) {
-        const float c = above_minus_inf(z);
-        return c * sigmoid2(c * __builtin_fmaf(kTanhC * kTanhA, c * c, kTanhC));
-    }
-    if constexpr (kAct == kActSilu) {
-        const float c = above_minus_inf(z);
-        return c * sigmoid2(c * kLog2e);
-    }
+    if constexpr (kAct == kActGelu)
+        return share(z, Normal(z).phi);
+    if constexpr (kAct == kActGeluTanh)
+        return share(z, sigmoid2(z * __builtin_fmaf(kTanhC * kTanhA, z * z, kTanhC)));
+    if constexpr (kAct == kActSilu)
+        return share(z, sigmoid2(z * kLog2e));
     return z;
 }
 // Slopes are constant to fp32's last place beyond +-100; z^2 stays finite there.

@@ -23,7 +23,8 @@ struct F32Stage {
     static constexpr int kPasses = kRB <= 4 ? 1 : 2, kBlocks = kRB / kPasses, kRows = 16 * kBlocks;
     static constexpr int kBytes = kRows * kSide * 4;
     static constexpr int kLanes = kSide / 8;                           // lanes of a row on the way back
-    static constexpr int kTurn = kB == 6 ? 3 : 4;                      // groups of a lane in a turn
+    // groups of a lane in a turn: what the registers hold, of which 128-tiles have 256
+    static constexpr int kTurn = kB == 6 ? 3 : kB == 4 && kRB == 4 ? 2 : 4;
     static constexpr int kTurnRows = 64 * kTurn / kLanes, kTurns = kRows / kTurnRows;
     static constexpr bool kAligned = 64 % kLanes == 0;                 // a lane's groups share their columns
     static_assert(64 * kTurn % kLanes == 0 && kRows % kTurnRows == 0, "whole turns");
@@ -189,10 +190,32 @@ struct Epilogue {
                         v[u][e] += __builtin_bit_cast(float, a);
                         v[u][4 + e] += __builtin_bit_cast(float, b);
                     }
+            // back to where they came from, and out in whole lines: a lane's 32 bytes would be
+            // two stores of half lines (16384 x 14336 x 4096 with a residual 1540 us so, 1488
+            // with the hint that nothing reads them soon)
 #pragma unroll
-            for (int u = 0; u < St::kTurn; ++u)
-                if (inside(turn, u))
-                    store8_32<true>(y.get(u), columns(u), v[u]);
+            for (int u = 0; u < St::kTurn; ++u) {
+                const int rl = local + (64 * u + lane) / St::kLanes, first = (col[u] - col0) >> 2;
+                *reinterpret_cast<f32x4_t *>(mine + St::place(rl, first)) = f32x4_t{v[u][0], v[u][1], v[u][2], v[u][3]};
+                *reinterpret_cast<f32x4_t *>(mine + St::place(rl, first + 1)) = f32x4_t{v[u][4], v[u][5], v[u][6], v[u][7]};
+            }
+            lanes_in_step();
+#pragma unroll
+            for (int u = 0; u < St::kTurn; ++u) {
+                const int rl = local + (64 * u + lane) / St::kLanes, i = (64 * u + lane) % St::kLanes;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int unit = half * St::kLanes + i, m = kWhole ? 4 : hold_v(p.N - col0 - 4 * unit);
+                    const u32x4_t w = *reinterpret_cast<const u32x4_t *>(mine + St::place(rl, unit));
+                    char *const to = y.get(u) + 16 * (half * St::kLanes - i);
+                    if (!inside(turn, u))
+                        continue;
+                    if (m >= 4)
+                        store16<true>(to, w);
+                    else
+                        store_tail32(to, m, Raw8{w, {0u, 0u, 0u, 0u}});
+                }
+            }
         } else {
             if (!kTrB && p.residual)
 #pragma unroll
