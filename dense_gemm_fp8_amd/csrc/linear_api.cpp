@@ -75,6 +75,8 @@ How how_to(int64_t M, int64_t N, int64_t K, bool transposed)
     if (M == 0 || N == 0 || K == 0 || (!transposed && M <= 16))
         return {How::kFewRows, 0, 0, 0};
     const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), steps = ceil_div(K, 64);
+    if (tiles >= int64_t(1) << 20)      // nothing else comes near, and the products below stay in range
+        return {How::kTiles, 0, 0, INT64_MAX / 4};
     const hkg::RowsGrid rows = hkg::rows_grid(M, N);
     const int64_t few = (transposed ? 6000 : 2000) + rows.step_ns * steps * ceil_div(rows.blocks(M, N), 256);
     const int64_t whole = 3000 + 600 * steps * ceil_div(tiles, 256);
@@ -220,7 +222,8 @@ int64_t hkg_linear_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 0 || N < 0 || K < 0 || K % 8)
         return HKG_ERR_SHAPE;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) / (kTile * 2))
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) / (kTile * 2) ||
+        (M > 16 && ceil_div(M, 128) * ceil_div(N, 128) >= (int64_t(1) << 24)))
         return HKG_ERR_SIZE;
     return M == 0 || N == 0 ? 0 : parts_bytes(how_to(M, N, K, false), M, N);
 }

@@ -220,9 +220,11 @@ def linear_backward(dy, x, W, z=None, activation=None, p=0.0, rng=None, dx=None,
     if need_dbias:
         if dbias is None:
             dbias = _ops._empty((N,), torch.float32, dy, stream)
+            pdb = dbias.data_ptr()
         elif tuple(dbias.shape) != (N,) or dbias.dtype is not torch.float32:
             raise ValueError("dbias must be a float32 tensor of shape (%d,)" % N)
-        pdb = _hkg._dev_ptr(dbias, "dbias")
+        else:
+            pdb = _hkg._dev_ptr(dbias, "dbias")
     need = _ops._check(_lib().hkg_linear_backward_workspace_bytes(M, N, K), "hkg_linear_backward_workspace_bytes")
     workspace, pws, nws = _ops._workspace(workspace, need, dy, stream)
     _ops._check(_on(dy).hkg_linear_backward(M, N, K, code, pdy, dy_code, lddy, px, ldx, pw, ldw, pz, ldz, act, opts, pdx, lddx,

@@ -99,6 +99,7 @@ typedef struct {
  *   epilogue  NULL: y = x W^T
  *   y         [M][N] of `type` or fp32 (y_type), rows ldy elements apart; may be
  *             the residual itself (the same pitch), else must not overlap it
+ * 2^24 tiles of 128 x 128 results, and M or N of 2^31, are refused (HKG_ERR_SIZE).
  * Sums and everything after them are fp32; y and z are each rounded once (z is
  * rounded to be kept, act takes it unrounded).  K == 0 is z = bias.
  */
@@ -116,7 +117,10 @@ int hkg_linear(int64_t M, int64_t N, int64_t K, int32_t type, const void *x, int
  *   z           of `type`; unused, and may be NULL, with HKG_ACT_NONE
  *   dropout     NULL: none
  *   dx, dw      [M][K] and [N][K] of `type`; dbias [N] fp32.  Any may be NULL;
- *               W may be NULL with dx, x with dw
+ *               W may be NULL with dx, x with dw.  Which of them are asked for does not
+ *               change the others' bits
+ * M, N and K below 2^22 - 8, and together 2^23 tiles of 64 x 64 of the three matrices
+ * (HKG_ERR_SIZE).
  */
 int64_t hkg_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int hkg_linear_backward(int64_t M, int64_t N, int64_t K, int32_t type, const void *dy,

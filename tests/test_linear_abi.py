@@ -86,7 +86,8 @@ def linear(M=64, N=64, K=64, t=0, x=P[0], ldx=0, W=P[1], ldw=0, e=None, y=P[2], 
     (dict(e=epilogue(z=P[3], ldz=63)), OPTS), (dict(ldy=-1), OPTS),
     (dict(K=1 << 22), SIZE), (dict(ldx=1 << 22), SIZE), (dict(ldw=1 << 40), SIZE), (dict(M=1 << 31), SIZE),
     (dict(N=1 << 31), SIZE), (dict(ldy=1 << 31), SIZE), (dict(ldy=(1 << 63) - 1), SIZE), (dict(K=(1 << 62)), SIZE),
-    (dict(N=(1 << 63) - 1), SIZE), (dict(K=0, N=1 << 31), SIZE),
+    (dict(N=(1 << 63) - 1), SIZE), (dict(K=0, N=1 << 31), SIZE), (dict(M=1 << 18, N=1 << 21), SIZE),
+    (dict(M=(1 << 31) - 1, N=(1 << 31) - 1, ldx=64, ldw=64), SIZE),
     (dict(y=P[0]), OVERLAP), (dict(y=P[1] + 64), OVERLAP), (dict(e=epilogue(z=P[2] + 16)), OVERLAP),
     (dict(e=epilogue(z=P[0])), OVERLAP), (dict(e=epilogue(bias=P[2] + 4)), OVERLAP),
     (dict(e=epilogue(r=P[2] + 2)), OVERLAP), (dict(e=epilogue(r=P[2], ldr=72)), OVERLAP),
