@@ -5,6 +5,13 @@
 // holds 8 consecutive columns, so z, the residual and y are whole lines of their rows,
 // one call of the generator serves a lane's 8 elements, and the code that handles 8
 // elements stands in a loop instead of once for each of a lane's 256 accumulators.
+//
+// Bound by the matrix cores at the power-capped clock: 8192 x 4096 x 14336 with bias,
+// residual and dropout 633-680 us (1.42-1.52 PFLOPS), the cores busy 82 % of the launch.
+// With 64 K steps a tile instead of 224 the epilogue counts: 16384 x 14336 x 4096 with bias,
+// gelu_tanh and z 1395-1614 us, busy 73 %, a tenth of it the epilogue (60 cycles of vector
+// instructions an element, two stores), beside which nothing runs: a 256-tile's ring of 160
+// KB of LDS leaves one workgroup a compute unit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

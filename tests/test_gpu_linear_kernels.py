@@ -127,3 +127,17 @@ def test_operands_beyond_two_gigabytes():
     y = hkg.linear(x, W)
     want, tol, _, _ = ref.linear(f64(x[rows]), f64(W))
     close(y[rows], want, tol, "y")
+
+
+@pytest.mark.parametrize("M,N,K", [(2048, 64, 64), (1500, 72, 72), (500, 1000, 768), (1200, 1000, 776), (4100, 300, 264)])
+def test_a_gradient_has_the_same_bits_whichever_others_are_asked_for(M, N, K):
+    x, W, dy, z = normal(1, M, K), normal(2, N, K), normal(3, M, N), normal(4, M, N)
+    def gradients(*need):
+        return hkg.linear_backward(dy, x, W, z=z, activation="silu", p=0.2, rng=(3, 4), need_dx=need[0], need_dw=need[1],
+                                   need_dbias=need[2])
+    every = gradients(True, True, True)
+    for need in ((True, True, False), (True, False, True), (False, True, True), (True, False, False), (False, True, False),
+                 (False, False, True)):
+        for got, want, asked in zip(gradients(*need), every, need):
+            assert (got is not None) == asked
+            assert got is None or torch.equal(got, want), need
