@@ -113,6 +113,8 @@ int hkg_linear(int64_t M, int64_t N, int64_t K, int32_t type, const void *x, int
  *   dz = D(dy) act'(z),  dx = dz W,  dw = dz^T x,  dbias = sums of dz over rows
  * (the residual's gradient is dy itself).  The operands of the two products are of
  * `type`, so dz is rounded to it for them; dbias sums dz unrounded, in a fixed order.
+ * fp16 holds no number beyond 65504: a larger dz, dx or dw (or y or z of the forward
+ * pass) becomes infinity, and dz below 2^-25 zero, so a loss is scaled to suit it.
  *   dy          [M][N] of `type` or fp32 (dy_type), rows lddy elements apart
  *   z           of `type`; unused, and may be NULL, with HKG_ACT_NONE
  *   dropout     NULL: none
