@@ -141,3 +141,40 @@ def test_a_gradient_has_the_same_bits_whichever_others_are_asked_for(M, N, K):
         for got, want, asked in zip(gradients(*need), every, need):
             assert (got is not None) == asked
             assert got is None or torch.equal(got, want), need
+
+
+def test_calls_at_once_on_two_streams_and_from_two_threads():
+    """Every call has a workspace of its own: products whose K is split over workgroups, and
+    gradients, side by side."""
+    import threading
+    sizes = ((100, 1024, 4096), (300, 520, 776))
+    data = [(normal(4 * i + 1, M, K), normal(4 * i + 2, N, K), normal(4 * i + 3, M, N)) for i, (M, N, K) in enumerate(sizes)]
+
+    def calls(x, W, dy, stream=None):
+        return (hkg.linear(x, W, activation="silu", p=0.1, rng=(1, 2), stream=stream),
+                *hkg.linear_backward(dy, x, W, p=0.1, rng=(1, 2), stream=stream))
+    want = [calls(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(calls(*data[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    threaded = [[], []]
+
+    def work(i):
+        for _ in range(10):
+            threaded[i].append(calls(*data[i], stream=streams[i]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for runs in (got, threaded):
+        for i in range(2):
+            assert len(runs[i]) == 10
+            for one in runs[i]:
+                for u, v in zip(one, want[i]):
+                    assert torch.equal(u, v)
