@@ -76,8 +76,8 @@ __global__ __launch_bounds__(256, kT == 128 ? 2 : 1) void mx4_tile_kernel(const 
     mx4_tile<kT>(o, p, blockIdx.x, smem);
 }
 
-// Two products: the first `first` workgroups (a multiple of 8: both orders count on
-// workgroup b running on XCD b mod 8) are product 0's tiles, padded, the rest product 1's.
+// Two products: the first `first` workgroups (a multiple of 8: both orders count on the
+// workgroups of one b mod 8 sharing an XCD) are product 0's tiles, padded, the rest product 1's.
 struct TilePair {
     TileOperands o[2];
     Mx4GemmParams p[2];

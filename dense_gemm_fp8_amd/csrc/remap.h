@@ -2,8 +2,10 @@
 //
 // HipKittens L2 note: section 2 (Pillar 3, non-programmable cache), section 7
 // (code citation 5, Algorithm 1 "XCD swizzle"), section 5 (Table 4: window W,
-// chunk C).  The hardware hands workgroup b of a launch to XCD b mod 8, so
-// neighbouring ids land on different L2 caches.  The remap
+// chunk C).  The hardware hands the workgroups of a launch to the 8 XCDs in turn, from
+// one that its queue decides: those of one residue b mod 8 share an XCD, and
+// neighbouring ids land on different L2 caches.  (Below, an XCD's number is that
+// residue.)  The remap
 //   1. takes the flat id b of the Gm x Gn grid;
 //   2. splits [0, G) at multiples of one cycle of 8*C ids;
 //   3. inside full cycles gives the j-th workgroup an XCD receives the id

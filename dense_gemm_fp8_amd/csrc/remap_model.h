@@ -7,7 +7,8 @@
 // maximise it.  The pages print the equation and measured hit rates but no
 // way to predict the hit rates of an order before running it; this model
 // predicts them from the launch itself:
-//  - dispatch: workgroup b runs on XCD b mod 8 (checked on the GPU); each XCD
+//  - dispatch: workgroup b runs on XCD b mod 8, XCDs counted from the one that
+//    workgroup 0 runs on (checked on the GPU); each XCD
 //    runs `per_xcd` workgroups at a time (32 CUs x workgroups per CU), so
 //    round r of XCD x holds workgroups x + 8 (per_xcd r + j), j < per_xcd;
 //  - L2 (one per XCD): the tiles an XCD holds at once stream the same K

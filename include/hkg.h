@@ -312,7 +312,8 @@ int hkg_launch_plan(int64_t M, int64_t N, int64_t K, int32_t dtype, const hkg_ge
  *               the previous round when that round's panels fit the cache)
  *   eq1_bw_tbs  5.99 * llc_hit + 17.05 * l2_hit (TB/s; the constants fit every
  *               row of the note's Table 4, section 5)
- * Workgroup b is taken to run on XCD b mod 8 (hkg_probe_xcd checks it), and
+ * The workgroups of one residue b mod 8 are taken to run on one XCD, those of
+ * another on another (hkg_probe_xcd checks it), and
  * rounds of 8 * per_xcd workgroups to run together; the first 8 rounds are
  * simulated.  An analysis aid: the default order (hkg_default_remap) is the
  * measured rule, which this model's L2 term explains.
@@ -401,8 +402,11 @@ int hkg_remap_tiles_device(int64_t Gm, int64_t Gn, int32_t W, int32_t C, int32_t
 /*
  * Diagnostic of the premise behind the grid remap: the remap (HipKittens L2
  * note, section 2 Pillar 3 and section 7 code citation 5, Algorithm 1's
- * "de-interleave round-robin" step) assumes that the hardware hands
- * workgroup b of a launch to XCD b mod 8.  This launches `workgroups`
+ * "de-interleave round-robin" step) assumes that the hardware hands the
+ * workgroups of a launch to the 8 XCDs in turn: workgroup b to XCD
+ * (first + b) mod 8.  `first` is the hardware queue's: 0 while a process has
+ * few queues, any other once streams share them, on every stream then; the
+ * remap's result does not depend on it.  This launches `workgroups`
  * workgroups of 256 threads; each records where it ran:
  *   out[2*b]     the XCC_ID hardware register (bits 3:0: the XCD)
  *   out[2*b + 1] the HW_ID hardware register (wave slot, SIMD, CU, shader

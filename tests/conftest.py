@@ -21,7 +21,19 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU test")
 
 
+# Tests that expect a launch to begin at XCD 0.  The hardware queue decides where it begins:
+# at 0 until a process has used more streams than there are queues, at any XCD from then on
+# (tests/test_gpu_xcd.py), so these run before every other test.
+ON_THE_FIRST_QUEUE = ("test_workgroup_b_runs_on_xcd_b_mod_8", "test_time_record")
+
+
+def first_queue_first(items):
+    """`items` with the tests of ON_THE_FIRST_QUEUE in front, otherwise in their order."""
+    return sorted(items, key=lambda i: i.name.split("[")[0] not in ON_THE_FIRST_QUEUE)
+
+
 def pytest_collection_modifyitems(config, items):
+    items[:] = first_queue_first(items)
     named = [i for i in items if i.nodeid.endswith(VALID_CALLS_ON_MADE_UP_ADDRESSES)]
     if not named:
         return
