@@ -241,6 +241,13 @@ __device__ __forceinline__ void drop8(const DropoutParams &d, const u32x4_t &n, 
 // ---- activations ------------------------------------------------------------------
 // v_exp_f32 and v_rcp_f32, both within a unit of fp32's last place: a quarter of the
 // usual rate each, where the library's functions take ten times as long.
+//
+// An exponential magnifies its argument's rounding: e^u of an fp32 u is off by up to |u|
+// 2^-24, and u reaches 88 where results are still numbers of fp32.  Results of 16 bits are
+// formed so (kWide = false: within 2^-15 of the value, where they are rounded by 2^-8 or
+// 2^-11), results of 32 bits from arguments of two parts (kWide: within 2^-20).  16384 x 14336 x
+// 4096 with gelu, gelu_tanh and silu into fp32 1518, 1459 and 1410 us so, 1423, 1371 and 1365 as
+// 16-bit results are formed; 1 x 14336 x 4096 21.1 either way.
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp_of(float x) { return __builtin_amdgcn_rcpf(x); }
 constexpr float kLog2e = 1.44269504f;
@@ -255,33 +262,78 @@ __device__ __forceinline__ float share(float z, float s) { return __builtin_fmax
 // 1 / (1 + 2^-u): 2^-u may be infinity, which gives 0.
 __device__ __forceinline__ float sigmoid2(float u) { return rcp_of(1.0f + exp2_of(-u)); }
 
-// g = exp(-z^2 / 2) and Phi(z).  Phi(-|z|) = g k Q(k) with k = 1 / (1 + 0.24 |z|), Q a
-// polynomial fitted for the smallest relative error over |z| < 40 (4.3e-7): no
-// cancellation on the left, where Phi is small.
+// h(a) = Phi(-a) exp(a^2 / 2), a >= 0, from k = 1 / (3.25 + a): k Q(k), Q a polynomial fitted for
+// the smallest relative error over a < 14 (1.3e-7, 1.5e-7 with these fp32 coefficients), beyond
+// which z Phi(z) is below 2^-126.  No cancellation on the left, where Phi is small.
+__device__ __forceinline__ float phi_over_exp(float k)
+{
+    float q = 451.416382f;
+    q = __builtin_fmaf(q, k, -562.613159f);
+    q = __builtin_fmaf(q, k, 199.171753f);
+    q = __builtin_fmaf(q, k, -9.12508869f);
+    q = __builtin_fmaf(q, k, 12.8180742f);
+    q = __builtin_fmaf(q, k, 3.63388824f);
+    q = __builtin_fmaf(q, k, 1.30244911f);
+    q = __builtin_fmaf(q, k, 0.398862779f);
+    return q * k;
+}
 struct Normal {
-    float g, phi;
+    float g, phi;                  // exp(-z^2 / 2), Phi(z)
     __device__ __forceinline__ explicit Normal(float z)
     {
-        const float a = __builtin_fabsf(z), k = rcp_of(__builtin_fmaf(0.24f, a, 1.0f));
         g = exp2_of(z * z * (-0.5f * kLog2e));
-        float q = -0.05299046263f;
-        q = __builtin_fmaf(q, k, 0.15278859437f);
-        q = __builtin_fmaf(q, k, -0.0656934455f);
-        q = __builtin_fmaf(q, k, 0.11838012934f);
-        q = __builtin_fmaf(q, k, 0.06340177357f);
-        q = __builtin_fmaf(q, k, 0.09283750504f);
-        q = __builtin_fmaf(q, k, 0.09552230686f);
-        q = __builtin_fmaf(q, k, 0.09575378895f);
-        const float tail = g * (q * k);
+        const float tail = g * phi_over_exp(rcp_of(__builtin_fabsf(z) + 3.25f));
         phi = z < 0.0f ? tail : 1.0f - tail;
     }
 };
 
-template <int kAct>
+// The shares for results of 32 bits, |z| at most 100: 2^t with t a whole number and a rest r,
+// and what z's powers and the constants lose in fp32 (x_lo, kXLo) carried along.
+// (Written so that constants are inline or single literals: more scalar registers for them
+// would spill out of the 256-tiles' epilogue.)
+__device__ __forceinline__ float exp2_of(float n, float r) { return __builtin_amdgcn_ldexpf(exp2_of(r), (int)n); }
+constexpr float kLog2eLo = 1.925963033e-8f;
+constexpr float kTanhCube = 0.102943242f, kTanhCubeLo = -2.01619832e-09f;   // 2 sqrt(2 / pi) 0.044715 log2 e
+constexpr float kTanhSum = 22.359375f, kTanhSumLo = 0.00448500225f;           // 1 / 0.044715; kTanhSum has 11 bits
+
+__device__ __forceinline__ float silu_share(float z)
+{
+    const float n = __builtin_rintf(z * kLog2e), r = __builtin_fmaf(z, -kLog2eLo, __builtin_fmaf(z, -kLog2e, n));
+    return rcp_of(1.0f + exp2_of(-n, r));
+}
+__device__ __forceinline__ float gelu_tanh_share(float z)
+{
+#pragma clang fp contract(off)   // s and p as rounded: what they lose is in s_lo and p_lo
+    // t = -A z (z^2 + 1 / 0.044715), the sum u and the product p in two parts; u - kTanhSum is
+    // exact, that constant's last bit being above u's
+    const float s = z * z, s_lo = __builtin_fmaf(z, z, -s), u = s + kTanhSum, u_lo = (s - (u - kTanhSum)) + (s_lo + kTanhSumLo);
+    const float p = z * u, p_lo = __builtin_fmaf(z, u_lo, __builtin_fmaf(z, u, -p)), n = __builtin_rintf(p * kTanhCube);
+    const float r = __builtin_fmaf(p_lo, -kTanhCube, __builtin_fmaf(p, -kTanhCubeLo, __builtin_fmaf(p, -kTanhCube, n)));
+    return rcp_of(1.0f + exp2_of(-n, r));
+}
+// k Q(k) turns an error of k into one three times as large, so what k misses goes in by the
+// derivative: h' = a h - 1 / sqrt(2 pi), and k stands for a number that is `off` below a.
+__device__ __forceinline__ float gelu_share(float z)
+{
+    const float s = z * z, s_lo = __builtin_fmaf(z, z, -s), n = __builtin_rintf(s * (0.5f * kLog2e));
+    const float r = __builtin_fmaf(s_lo, -0.5f * kLog2e, __builtin_fmaf(s, -0.5f * kLog2eLo, __builtin_fmaf(s, -0.5f * kLog2e, n)));
+    const float a = __builtin_fabsf(z), d = a + 3.25f, d_lo = a - (d - 3.25f), k = rcp_of(d), h = phi_over_exp(k);
+    const float off = __builtin_fmaf(-d, __builtin_fmaf(-d, k, 1.0f), d_lo);
+    const float tail = exp2_of(-n, r) * __builtin_fmaf(off * a, h, __builtin_fmaf(off, -0.39894228f, h));
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+template <int kAct, bool kWide>
 __device__ __forceinline__ float act_of(float z)
 {
     if constexpr (kAct == kActRelu)
         return z <= 0.0f ? 0.0f : z;
+    if constexpr (kWide && kAct != kActNone) {
+        // the share is constant beyond +-100, where z's powers are finite; a NaN's is lost here
+        const float c = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f);
+        const float v = share(z, kAct == kActGelu ? gelu_share(c) : kAct == kActGeluTanh ? gelu_tanh_share(c) : silu_share(c));
+        return z != z ? z : v;
+    }
     if constexpr (kAct == kActGelu)
         return share(z, Normal(z).phi);
     if constexpr (kAct == kActGeluTanh)
@@ -290,7 +342,8 @@ __device__ __forceinline__ float act_of(float z)
         return share(z, sigmoid2(z * kLog2e));
     return z;
 }
-// Slopes are constant to fp32's last place beyond +-100; z^2 stays finite there.
+// Slopes, within 2^-19.  They are constant to fp32's last place beyond +-100; z^2 stays finite
+// there.
 template <int kAct>
 __device__ __forceinline__ float slope_of(float z)
 {
@@ -324,17 +377,27 @@ __device__ __forceinline__ void with_activation(int act, F &&f)
     default: break;
     }
 }
-__device__ __forceinline__ void act8(int act, float (&v)[8])
+// And whether it is evaluated for a result of 32 bits.
+template <class F>
+__device__ __forceinline__ void with_evaluation(int act, int f32, F &&f)
 {
-    with_activation(act, [&](auto a) __attribute__((always_inline)) {
+    if (f32)
+        with_activation(act, [&](auto a) __attribute__((always_inline)) { f(a, std::true_type{}); });
+    else
+        with_activation(act, [&](auto a) __attribute__((always_inline)) { f(a, std::false_type{}); });
+}
+__device__ __forceinline__ void act8(int act, int f32, float (&v)[8])
+{
+    with_evaluation(act, f32, [&](auto a, auto wide) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = act_of<decltype(a)::value>(v[e]);
+            v[e] = act_of<decltype(a)::value, decltype(wide)::value>(v[e]);
     });
 }
-__device__ __forceinline__ float act1(int act, float v)
+__device__ __forceinline__ float act1(int act, int f32, float v)
 {
-    with_activation(act, [&](auto a) __attribute__((always_inline)) { v = act_of<decltype(a)::value>(v); });
+    with_evaluation(act, f32, [&](auto a, auto wide)
+                    __attribute__((always_inline)) { v = act_of<decltype(a)::value, decltype(wide)::value>(v); });
     return v;
 }
 

@@ -176,12 +176,12 @@ struct Epilogue {
             z.next();
         }
         if constexpr (!kTrB)
-            with_activation(p.act, [&](auto a) __attribute__((always_inline)) {
+            with_evaluation(p.act, p.y_f32, [&](auto a, auto wide) __attribute__((always_inline)) {
     #pragma unroll
                 for (int u = 0; u < St::kTurn; ++u)
     #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[u][e] = act_of<decltype(a)::value>(v[u][e]);
+                        v[u][e] = act_of<decltype(a)::value, decltype(wide)::value>(v[u][e]);
             });
         if (!kTrB && p.drop.below > 0)
 #pragma unroll
@@ -479,7 +479,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinearParams p, 
     }
     if (p.z)
         store8_16<T>(element_at(p.z, row * p.ldz + col, 2), n, v);
-    act8(p.act, v);
+    act8(p.act, p.y_f32, v);
     if (p.drop.below > 0)
         drop8(p.drop, Key(p.drop).numbers(p.row0 + row, (p.col0 + col) >> 3), v);
     if (p.residual)

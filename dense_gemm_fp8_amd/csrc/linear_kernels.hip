@@ -286,7 +286,7 @@ __device__ __forceinline__ void few_rows_block(const LinearParams &p, int block,
             v += p.bias_f32 ? static_cast<const float *>(p.bias)[col] : T::low(static_cast<const uint16_t *>(p.bias)[col]);
         if (p.z)
             static_cast<uint16_t *>(p.z)[row * p.ldz + col] = (uint16_t)T::pack2(v, 0.f);
-        v = act1(p.act, v);
+        v = act1(p.act, p.y_f32, v);
         if (p.drop.below > 0)
             v = kept(key.numbers(p.row0 + row, (p.col0 + col) >> 3), col & 7, p.drop.below) ? v * p.drop.scale : 0.0f;
         const int64_t at = row * p.ldy + col, from = row * p.ldr + col;

@@ -31,7 +31,9 @@ enum { HKG_T_F16 = 2 };
  *   HKG_ACT_GELU       z Phi(z), Phi the normal distribution function
  *   HKG_ACT_GELU_TANH  z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
  *   HKG_ACT_SILU       z / (1 + exp(-z))
- * Evaluated in fp32, to a few units of its last place.  At -infinity all but
+ * Evaluated within 2^-20 of the value for a y in fp32, and within 2^-15 of it for one
+ * of 16 bits, which is then rounded by up to 2^-8 (bf16) or 2^-11 (fp16); a value below
+ * 2^-116 in magnitude may become 0.  Slopes within 2^-19.  At -infinity all but
  * HKG_ACT_NONE are 0, with slope 0; a NaN stays one.
  */
 enum {

@@ -110,17 +110,19 @@ def slope(z, name):
         return (1.0 + c / (1.0 + np.exp(c))) / (1.0 + np.exp(-c))
 
 
-def act_error(z, name):
-    """A few units of fp32's last place, and the exponential's argument, which is rounded
-    to 2^-24 of itself: at most z^2 for all three (but for relu and none, which are exact)."""
+def act_error(z, name, y_type="fp32"):
+    """What include/hkg_linear.h states (none and relu are exact).  fp32: an exponential and a
+    reciprocal, each within a unit of the last place (2^-23), and at most ten roundings of
+    2^-24 (gelu's polynomial and products), the exponential's argument being below 1.  16 bits: the
+    exponential's argument goes through at most five roundings of 2^-24 in fp32, and is at
+    most 88 where the result is not 0."""
     z = np.asarray(z, dtype=np.float64)
     if name in (None, "relu"):
         return np.zeros_like(z)
-    c = np.clip(z, -40.0, 40.0)
-    return np.abs(act(z, name)) * (2.0 ** -20 + c * c * 2.0 ** -22) + 1e-35
+    return np.abs(act(z, name)) * (2.0 ** -20 if y_type == "fp32" else 2.0 ** -15) + 2.0 ** -116
 
 
-SLOPE_ERROR = 2.0 ** -19              # absolute: a few roundings of terms up to 1.2
+SLOPE_ERROR = 2.0 ** -19              # absolute, as stated: a few roundings of terms up to 1.2
 STEEPEST = 1.13                       # no slope exceeds it
 
 
@@ -146,7 +148,7 @@ def linear(x, W, bias=None, activation=None, residual=None, p=0.0, rng=None, y_t
         z = z + bias
         err = err + 2.0 ** -24 * np.abs(z)
     v = act(z, activation)
-    e = STEEPEST * err + act_error(z, activation)
+    e = STEEPEST * err + act_error(z, activation, y_type)
     if below(p):
         k = keep(*v.shape, p, rng, row0)
         v = np.where(k, v * scale(p), 0.0)
