@@ -353,7 +353,8 @@ struct TileLoop {
     // compiler else waits for all loads to LDS before each ds_read_b64_tr_b16 (a gradient of
     // 8192 x 14336 x 4096 2600 us instead of 650), where the loop waits for those that it
     // needs.  M0 holds a load's LDS address, a wait state before it at least; nothing else
-    // in these kernels uses it.
+    // in these kernels writes it, which the load's statement cannot say: tests/test_linear_m0.py
+    // reads it off the listing.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
     __device__ __forceinline__ void set_m0(int lds_off, int v) const
