@@ -139,7 +139,11 @@ struct BackwardLayout {
         x = how_to(M, K, N, true);
         w = how_to(N, K, M, true);
         // both by the kernel for few rows are one launch, with the bias's sums: worth 5 us of
-        // the host's and the GPU's time (500 x 1000 x 768 in fp16 27.6 us a call in four launches)
+        // the host's and the GPU's time (500 x 1000 x 768 in fp16 27.6 us a call in four launches,
+        // 21.8 in two).  In replayed graphs, where the host's part is gone, in us apart and
+        // together: 150 x 140 x 72 16.0 and 7.2, 300 x 300 x 304 19.2 and 8.8, 256 x 512 x 512 13.8 and
+        // 10.0, 768 x 768 x 768 24.3 and 22.5; 500 x 1000 x 768 20.7 and 21.4, 400 x 1200 x 800 24.1 and
+        // 25.4, 64 x 2048 x 512 15.0 and 16.8, 128 x 1024 x 1024 14.5 and 17.1
         if (x.few_over + w.few_over < 5000 && x.few_over < 4000 && w.few_over < 4000)
             x = w = {How::kFewRows, 0, 0, 0};
         // the kernel for few rows takes transposed copies, tiles the matrices themselves

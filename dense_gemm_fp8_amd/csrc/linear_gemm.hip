@@ -512,9 +512,12 @@ TransposableOperands operands(const TileGrid &g, const LinearParams &p)
     return o;
 }
 
-// K steps from which two groups of waves gain more than their exchange costs: 1111 x 2777 x
-// 1184 (19 steps) 17.1 us against 15.8, 1024 x 4096 x 4096 40.7 against 37.1; a gradient of 1024 x
-// 1024 with K = 64 7.0 against 8.7.
+// K steps from which two groups of waves gain more than their exchange costs, in replayed graphs
+// (us, one group / two).  1000 x 4096: 8 steps 9.5 / 9.4, 12 11.3 / 11.3, 16 13.0 / 13.1, 24 18.4 /
+// 17.3, 64 38.5 / 33.2; 1000 x 2000: 8 10.0 / 9.2, 16 12.5 / 11.5, 64 26.6 / 26.7.  Operands with K
+// along their columns gain later, a gradient dx of 1000 x 4096: 4 steps 10.1 / 11.3, 8 12.4 / 13.4,
+// 12 14.8 / 16.2, 16 17.8 / 18.1, 24 22.8 / 23.0, 32 27.3 / 26.3; dw of 1000 x 4096: 8 13.2 / 14.0, 16
+// 19.5 / 19.4, 32 28.8 / 27.8.
 constexpr int kTwoFrom = 12;
 
 template <class T, class Mma, bool kTrA, bool kTrB>
@@ -544,7 +547,10 @@ hipError_t tiles_as(const TileGrid &g, const LinearParams &p, hipStream_t stream
 
 // Parts of many steps by two groups of waves: 128 x 8192 x 8192 in 4 parts of 32 steps 40.4 us
 // against 36.9, 512 x 4096 x 14336 in 2 of 112 82.9 against 76.3; of 8 steps (128 x 4096 x 4096
-// in 8) 16.9 against 18.4.
+// in 8) 16.9 against 18.4.  1024 x 1024 in 4 parts with operands that the caches hold (one group /
+// two): 16 steps 22.0 / 23.8, 32 31.8 / 34-38, 48 37.2 / 36.7, 64 45.0 / 42.3, 128 77.2 / 70.1; a
+// gradient dx, with dz's pass: 32 39.2 / 43.1, 48 47.2 / 45.6, 64 57.2 / 55.6, 128 100 / 93.5; dw 32
+// 39.2 / 41.8, 48 47.5 / 47.1, 64 57.9 / 56.5, 96 80 / 78, 128 101 / 103.
 template <class Mma, bool kTrA, bool kTrB>
 void part_launch(unsigned blocks, const TransposableOperands &o, int steps, float *parts, hipStream_t stream)
 {

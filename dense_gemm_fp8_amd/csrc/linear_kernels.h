@@ -1,6 +1,7 @@
 // linear_kernels.h -- launch interface between the entry points of hkg_linear.h
-// (linear_api.cpp) and their gfx950 kernels (linear_kernels.hip).  Internal to
-// libhkg; all argument checks are done by the caller.
+// (linear_api.cpp) and their gfx950 kernels (linear_kernels.hip; tiles and products
+// split along K: linear_gemm.hip).  Internal to libhkg; all argument checks are done by the
+// caller.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,21 +77,21 @@ inline int64_t linear_parts_bytes(int64_t M, int64_t N, int64_t splits)
 }
 hipError_t launch_linear_split(bool f16, const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p,
                                hipStream_t stream);
-// The kernel for few rows: workgroups of 16 mb rows x 16 nb columns, in runs of ks 32-k
-// steps, and about what 64 k take, in ns, for each 256 workgroups.  The smallest blocks whose
+// The kernel for few rows: workgroups of 16 mb rows x 16 nb columns, and about what 64 k
+// take, in ns, for each 256 workgroups.  The smallest blocks whose
 // grid still is one workgroup for each compute unit, since what bounds it is how much each
 // unit has in flight; one column block and long runs always for up to 16 rows.  Replayed
-// graphs over weights in turn, us, for mb nb ks = 122 / 114: 1 x 4096 x 4096 11.5 / 7.6, 1 x
+// graphs over weights in turn, us, for mb, nb and 32-k steps of a run = 122 / 114: 1 x 4096 x 4096 11.5 / 7.6, 1 x
 // 14336 x 4096 26.0 / 23.3, 16 x 8192 x 8192 33.6 / 28.6; 222 / 212: 32 x 4096 x 4096 13.9 /
 // 10.3, 32 x 14336 x 4096 29.2 / 32.7; 422 / 412: 64 x 4096 x 4096 16.7 / 13.5, 64 x 8192 x
 // 8192 39.0 / 46.0.
 struct RowsGrid {
-    int mb, nb, ks, step_ns;
+    int mb, nb, step_ns;
     int64_t blocks(int64_t M, int64_t N) const { return (M + 16 * mb - 1) / (16 * mb) * ((N + 16 * nb - 1) / (16 * nb)); }
 };
 inline RowsGrid rows_grid(int64_t M, int64_t N)
 {
-    constexpr RowsGrid one = {1, 1, 4, 130}, small = {2, 1, 2, 130}, wide = {2, 2, 2, 200}, tall = {4, 1, 2, 180}, large = {4, 2, 2, 240};
+    constexpr RowsGrid one = {1, 1, 130}, small = {2, 1, 130}, wide = {2, 2, 200}, tall = {4, 1, 180}, large = {4, 2, 240};
     if (M <= 16)
         return one;
     if (small.blocks(M, N) <= 256)
