@@ -77,14 +77,13 @@ inline int64_t linear_parts_bytes(int64_t M, int64_t N, int64_t splits)
 }
 hipError_t launch_linear_split(bool f16, const TileGrid &g, int splits, int steps, float *parts, const LinearParams &p,
                                hipStream_t stream);
-// The kernel for few rows: workgroups of 16 mb rows x 16 nb columns, and about what 64 k
-// take, in ns, for each 256 workgroups.  The smallest blocks whose
-// grid still is one workgroup for each compute unit, since what bounds it is how much each
-// unit has in flight; one column block and long runs always for up to 16 rows.  Replayed
-// graphs over weights in turn, us, for mb, nb and 32-k steps of a run = 122 / 114: 1 x 4096 x 4096 11.5 / 7.6, 1 x
-// 14336 x 4096 26.0 / 23.3, 16 x 8192 x 8192 33.6 / 28.6; 222 / 212: 32 x 4096 x 4096 13.9 /
-// 10.3, 32 x 14336 x 4096 29.2 / 32.7; 422 / 412: 64 x 4096 x 4096 16.7 / 13.5, 64 x 8192 x
-// 8192 39.0 / 46.0.
+// The kernel for few rows: workgroups of 16 mb rows x 16 nb columns, and about what 64 k take,
+// in ns, for each 256 workgroups.  The smallest blocks whose grid still is one workgroup for
+// each compute unit, since what bounds it is how much each unit has in flight; one column
+// block and long runs always for up to 16 rows.  Replayed graphs over weights in turn, us, for
+// mb, nb and the 32-k steps of a run = 122 / 114: 1 x 4096 x 4096 11.5 / 7.6, 1 x 14336 x 4096
+// 26.0 / 23.3, 16 x 8192 x 8192 33.6 / 28.6; 222 / 212: 32 x 4096 x 4096 13.9 / 10.3, 32 x 14336 x
+// 4096 29.2 / 32.7; 422 / 412: 64 x 4096 x 4096 16.7 / 13.5, 64 x 8192 x 8192 39.0 / 46.0.
 struct RowsGrid {
     int mb, nb, step_ns;
     int64_t blocks(int64_t M, int64_t N) const { return (M + 16 * mb - 1) / (16 * mb) * ((N + 16 * nb - 1) / (16 * nb)); }
